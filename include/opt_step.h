@@ -308,6 +308,148 @@ int opt_grad_norm(const opt_grad *grads, int64_t n, double *out, float max_norm,
 int opt_round_cast(const float *x, void *out, int64_t n, int32_t out_dtype, int32_t stochastic, uint64_t seed,
                    uint64_t offset, void *stream);
 
+/* ---- the training pass beside the step --------------------------------
+ * Operators that produce the gradients the step consumes, in the numerics of
+ * the rounding cast and of the FP8 states: dropout from the counter-based
+ * generator, the root-mean-square norm with the residual's addition, the cast
+ * to block-coded matrices, and their product.  They hold no workspace and
+ * take no lock: calls may overlap on any streams, threads and devices (each
+ * call runs on the current device) and be captured into graphs.
+ *
+ * Matrices are row-major: element (i, j) at p + i*ld + j, ld >= cols (in
+ * elements; any value for one row), p aligned to its element.  Nothing
+ * outside the cols elements of each of the rows is read or written.
+ * 0 <= rows, cols < 2^31 and rows*ld <= 2^46; a matrix of no elements is a
+ * no-op where nothing else is said.  Unless a name below says that two may be
+ * the same matrix (the same pointer and ld), buffers must not overlap.
+ *
+ * A block-coded matrix [rows, cols] holds OCP E4M3 codes and one power-of-two
+ * scale X for each row and each 128 consecutive columns from column 0 (the
+ * last block may be short): element (i, j) is value(codes[i*ld + j]) * X with
+ * X = 2^(scales[(j/128)*lds + i] - 127), and NaN where that byte is 255.
+ * Code rows are padded with zero codes to a multiple of 16 bytes.  */
+typedef struct {
+    uint8_t *codes;     /* device; ld bytes a row, of which roundup(cols, 16) are used */
+    int64_t ld;         /* a multiple of 16; codes 16-byte aligned                     */
+    uint8_t *scales;    /* device; [ceil(cols/128)][lds], the first rows bytes used    */
+    int64_t lds;        /* a multiple of 4, >= rows; scales 4-byte aligned             */
+} opt_codes;
+
+/* out[j] = residual[j] + (r_j >= T ? x[j] * s : 0) over n elements of dtype,
+ * with T = floor(65536 p + 1/2), s = 1/(1 - T/65536) rounded to binary32 and
+ * r_j the 16 random bits of element j: half j%2 (low first) of word (j%8)/2 of
+ * Philox4x32-10 keyed by `seed` with counter (j>>3 low, j>>35 | 2^31, offset
+ * low, offset high).  The mask is never stored: the backward pass is the same
+ * call on the gradient (residual NULL), with the same seed and offset.  Pass
+ * a new offset for each dropout.  The product and the sum are formed in
+ * binary32 and rounded once on store.  A dropped element is 0 (or the
+ * residual) whatever x holds; T = 65536 drops all.  0 <= p <= 1.
+ * residual: NULL for none; out may be x or residual.  index_base (>= 0, a
+ * multiple of 8): the index of element 0 within the whole tensor, so that a
+ * shard draws the mask of its part.  0 <= n <= 2^46, index_base + n <= 2^60. */
+int opt_dropout(const void *x, const void *residual, void *out, int64_t n, int32_t dtype, double p, uint64_t seed,
+                uint64_t offset, int64_t index_base, void *stream);
+
+/* The root-mean-square norm of each row, after the residual's addition:
+ *   h = x + residual, rounded to dtype (h = x without a residual);
+ *   r = 1/sqrt(mean(h^2) + eps), formed in binary64, rounded once to binary32;
+ *   y = (h * r) * weight in binary32, rounded once on store.
+ * y (in dtype) and q (block-coded, from the unrounded y, a scale for each row
+ * and 128 columns) are written as given; one at least is.  A row whose mean
+ * square and eps are both 0 gives NaN, as 0/0 does.  cols <= 32768. */
+typedef struct {
+    int64_t rows, cols;
+    int32_t dtype;             /* OPT_F32, OPT_BF16 or OPT_F16: x, residual, h, y      */
+    int32_t w_dtype;           /* the same three: weight                               */
+    const void *x;
+    int64_t ldx;
+    const void *residual;      /* or NULL                                              */
+    int64_t ldr;
+    const void *weight;        /* cols elements of w_dtype                             */
+    void *h;                   /* receives h, or NULL; may be x or residual            */
+    int64_t ldh;
+    void *y;                   /* receives y, or NULL; may be x or residual, not h     */
+    int64_t ldy;
+    opt_codes q;               /* receives y's codes and scales; codes NULL for none   */
+    double eps;                /* >= 0                                                 */
+} opt_norm;
+
+int opt_rms_norm(const opt_norm *a, void *stream);
+
+/* Its backward pass, from the h of the forward pass (what it stored, or x
+ * without a residual) and dy, the gradient of y:
+ *   g = dy * weight,  c = mean(g * h)  (both sums of a row in binary64),
+ *   dx = r * (g - h * (r^2 c)) + dh,   dweight = sum over rows of dy * (h * r).
+ * dx is the gradient of x and of the residual alike.  Sums over rows run in a
+ * fixed order (no atomics): binary32 within a workgroup's rows, binary64
+ * across workgroups.  cols <= 32768.  With rows = 0 dweight becomes 0 (or
+ * stays, with accumulate). */
+typedef struct {
+    int64_t rows, cols;
+    int32_t dtype;             /* OPT_F32, OPT_BF16 or OPT_F16: dy, h, dh, dx          */
+    int32_t w_dtype;           /* the same three: weight                               */
+    const void *dy;
+    int64_t lddy;
+    const void *h;
+    int64_t ldh;
+    const void *weight;
+    const void *dh;            /* gradient that reaches h by its other uses, or NULL   */
+    int64_t lddh;
+    void *dx;                  /* may be dy or dh                                      */
+    int64_t lddx;
+    float *dweight;            /* cols floats, or NULL for none                        */
+    int32_t accumulate;        /* 1: dweight += , 0: dweight =                         */
+    int32_t reserved;          /* 0 */
+    double eps;
+    void *workspace;           /* device scratch of opt_rms_norm_workspace bytes, 16-byte
+                                  aligned, free again when the call's work has run; NULL
+                                  without dweight                                      */
+    int64_t workspace_bytes;
+} opt_norm_grad;
+
+int opt_rms_norm_backward(const opt_norm_grad *a, void *stream);
+
+/* Bytes of workspace opt_rms_norm_backward needs for dweight at these sizes,
+ * or a negative status.  Host only. */
+int64_t opt_rms_norm_workspace(int64_t rows, int64_t cols);
+
+/* Codes of x in either layout, in one read of it: q is x's block-coded
+ * matrix [rows, cols], qt that of its transpose [cols, rows]; codes NULL
+ * leaves one out.  block_rows 1: a scale for each row of the coded matrix and
+ * 128 of its columns.  128: one scale for each 128 x 128 elements of x, stored
+ * for each row, the same in both layouts.  X is the smallest power of two, at
+ * least 2^-127, with A <= 448 X, A the block's largest magnitude, so nothing
+ * saturates; codes are x/X rounded to nearest-even.  A block of zeros has
+ * scale byte 0; one that holds a NaN or an infinity has 255 and zero codes. */
+typedef struct {
+    int64_t rows, cols;
+    const void *x;
+    int64_t ldx;
+    int32_t dtype;             /* OPT_F32, OPT_BF16 or OPT_F16 */
+    int32_t block_rows;        /* 1 or 128                     */
+    opt_codes q, qt;
+} opt_cast;
+
+int opt_block_cast(const opt_cast *a, void *stream);
+
+/* c[i, j] = sum over k of a[i, k] * b[j, k], plus c[i, j] if accumulate: the
+ * product of block-coded a [m, k] with the transpose of block-coded b [n, k],
+ * summed in binary32 in a fixed order and rounded once on store.  k counts
+ * code bytes and is a multiple of 16: a matrix whose columns are not one is
+ * given with its zero padding.  A layer's three products take the layouts of
+ * opt_block_cast: y = x W^T from q(x) and q(W); dx = dy W from q(dy) and
+ * qt(W); dW = dy^T x from qt(dy) and qt(x).  k = 0 gives 0 (or leaves c). */
+typedef struct {
+    int64_t m, n, k;
+    opt_codes a, b;
+    void *c;
+    int64_t ldc;
+    int32_t c_dtype;           /* OPT_F32, OPT_BF16 or OPT_F16 */
+    int32_t accumulate;        /* 1: c += , 0: c =             */
+} opt_product;
+
+int opt_block_matmul(const opt_product *a, void *stream);
+
 /* Test hook: the FP8/FP4 element codec of the state formats.  elem 0 = E4M3,
  * 1 = E2M1, 2 = unsigned E2M2.  For i < n: codes[i] = the code of x[i] in a
  * block whose absmax is A (A >= 0 or NaN), nearest-even if r is NULL, else

@@ -63,6 +63,36 @@ class OptGrad(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class OptCodes(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("ld", ctypes.c_int64), ("scales", ctypes.c_void_p), ("lds", ctypes.c_int64)]
+
+
+class OptNorm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("q", OptCodes), ("eps", ctypes.c_double)]
+
+
+class OptNormGrad(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dweight", ctypes.c_void_p),
+                ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32), ("eps", ctypes.c_double),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
+class OptCast(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("block_rows", ctypes.c_int32), ("q", OptCodes), ("qt", OptCodes)]
+
+
+class OptProduct(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("a", OptCodes), ("b", OptCodes),
+                ("c", ctypes.c_void_p), ("ldc", ctypes.c_int64), ("c_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -100,6 +130,12 @@ def lib():
             "opt_debug_mini_pack": ([i32, ctypes.c_float, vp, vp, vp, i64, vp], i32),
             "opt_round_cast": ([vp, vp, i64, i32, i32, ctypes.c_uint64, ctypes.c_uint64, vp], i32),
             "opt_step_1state": ([i32, T, i64, i32, H, vp], i32),
+            "opt_dropout": ([vp, vp, vp, i64, i32, ctypes.c_double, ctypes.c_uint64, ctypes.c_uint64, i64, vp], i32),
+            "opt_rms_norm": ([ctypes.POINTER(OptNorm), vp], i32),
+            "opt_rms_norm_workspace": ([i64, i64], i64),
+            "opt_rms_norm_backward": ([ctypes.POINTER(OptNormGrad), vp], i32),
+            "opt_block_cast": ([ctypes.POINTER(OptCast), vp], i32),
+            "opt_block_matmul": ([ctypes.POINTER(OptProduct), vp], i32),
             "opt_debug_mini_host": ([i32, ctypes.c_float, vp, vp, vp, vp, i64], i32),
         }
         for name, (args, res) in sig.items():
@@ -418,6 +454,198 @@ def opt_round_cast(x, out, stochastic=False, seed=0, offset=0, stream=None):
     _device_buffer(out, 2, x.numel(), "out")
     return _check(lib().opt_round_cast(_ptr(x), _ptr(out), x.numel(), _dtype_code(out), 1 if stochastic else 0,
                                        int(seed) & (2**64 - 1), int(offset) & (2**64 - 1), _stream(stream)))
+
+
+# ---- the training pass beside the step -------------------------------------
+# A matrix argument is a CUDA tensor on the current device: contiguous, of any
+# shape (its last dimension the columns), or 2-D with contiguous rows.  A
+# block-coded matrix is a pair (codes, scales) as block_buffers makes it.
+
+CODE_BLOCK = 128
+
+
+def _round_up(n, m):
+    return (n + m - 1) // m * m
+
+
+def block_buffers(rows, cols, device="cuda"):
+    """Zeroed buffers of a block-coded matrix [rows, cols]: E4M3 codes, uint8
+    [rows, cols rounded up to 16], and scale bytes, uint8 [ceil(cols/128),
+    rows rounded up to 4] (value(code) * 2^(byte - 127); see opt_codes in the
+    header)."""
+    import torch
+    return (torch.zeros(rows, _round_up(cols, 16), dtype=torch.uint8, device=device),
+            torch.zeros(_round_up(cols, CODE_BLOCK) // CODE_BLOCK, _round_up(rows, 4), dtype=torch.uint8, device=device))
+
+
+def _on_device(t, what, dev):
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.device.index != dev:
+        raise ValueError(f"{what} is on {t.device}, not on the current device cuda:{dev}")
+
+
+def _device():
+    import torch
+    return torch.cuda.current_device()
+
+
+def _sides(t, what):
+    """(rows, cols, leading dimension) of a matrix argument."""
+    if t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1):
+        rows, cols = t.shape
+        return rows, cols, t.stride(0) if rows > 1 else cols
+    if t.dim() >= 1 and t.is_contiguous():
+        cols = t.shape[-1]
+        return t.numel() // cols if cols else 0, cols, cols
+    raise ValueError(f"{what} must be contiguous, or 2-D with contiguous rows")
+
+
+def _like(t, what, like, rows, cols, dev):
+    """(pointer, leading dimension) of an optional matrix of the main one's
+    type and sides."""
+    if t is None:
+        return None, 0
+    _on_device(t, what, dev)
+    if t.dtype != like.dtype:
+        raise ValueError(f"{what} is {t.dtype}, not {like.dtype}")
+    r, c, ld = _sides(t, what)
+    if (r, c) != (rows, cols):
+        raise ValueError(f"{what} has {r} x {c} elements, not {rows} x {cols}")
+    return t.data_ptr(), ld
+
+
+def _coded(pair, what, rows, cols, dev):
+    """The opt_codes of a (codes, scales) pair that holds rows x cols."""
+    if pair is None:
+        return OptCodes()
+    q, s = pair
+    for t, part in ((q, "codes"), (s, "scales")):
+        _on_device(t, f"{what} {part}", dev)
+        if t.dim() != 2 or t.element_size() != 1 or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{what} {part} must be a 2-D tensor of bytes with contiguous rows")
+    if q.shape[0] != rows or q.shape[1] < _round_up(cols, 16):
+        raise ValueError(f"{what} codes must be [{rows}, >= {_round_up(cols, 16)}], got {list(q.shape)}")
+    if s.shape[0] < (cols + CODE_BLOCK - 1) // CODE_BLOCK or s.shape[1] < _round_up(rows, 4):
+        raise ValueError(f"{what} scales must be [>= {(cols + CODE_BLOCK - 1) // CODE_BLOCK}, >= {_round_up(rows, 4)}], got {list(s.shape)}")
+    return OptCodes(q.data_ptr(), q.stride(0) if rows > 1 else _round_up(cols, 16), s.data_ptr(),
+                    s.stride(0) if s.shape[0] > 1 else _round_up(rows, 4))
+
+
+def opt_dropout(x, out, p, seed=0, offset=0, residual=None, index_base=0, stream=None):
+    """out = residual + dropout(x): element j stays, divided by the share that
+    stays, where its 16 bits of the (seed, offset) stream reach 65536 p.  The
+    backward pass is the same call on the gradient, with no residual.  x, out
+    and residual are contiguous, of one type and size; out may be x or
+    residual.  index_base (a multiple of 8): the index of x's first element in
+    the whole tensor."""
+    dev = _device()
+    for t, what in ((x, "x"), (out, "out"), (residual, "residual")):
+        if t is not None:
+            _on_device(t, what, dev)
+            if not t.is_contiguous() or t.dtype != x.dtype or t.numel() != x.numel():
+                raise ValueError(f"{what} must be contiguous, of x's type and size")
+    return _check(lib().opt_dropout(x.data_ptr(), _ptr(residual), out.data_ptr(), x.numel(), _dtype_code(x), float(p),
+                                    int(seed) & (2**64 - 1), int(offset) & (2**64 - 1), int(index_base), _stream(stream)))
+
+
+def _weight(w, cols, dev):
+    _on_device(w, "weight", dev)
+    if w.numel() != cols or not w.is_contiguous():
+        raise ValueError(f"weight must be contiguous, of {cols} elements")
+    return w.data_ptr(), _dtype_code(w)
+
+
+def opt_rms_norm(x, weight, eps=1e-6, residual=None, h=None, y=None, codes=None, stream=None):
+    """h = x + residual (rounded to x's type), y = h / sqrt(mean(h^2) + eps) *
+    weight for each row.  h, y (of x's type) and codes (a block-coded pair)
+    receive what they name where they are given; y or codes must be."""
+    dev = _device()
+    _on_device(x, "x", dev)
+    rows, cols, ldx = _sides(x, "x")
+    pw, wd = _weight(weight, cols, dev)
+    pr, ldr = _like(residual, "residual", x, rows, cols, dev)
+    ph, ldh = _like(h, "h", x, rows, cols, dev)
+    py, ldy = _like(y, "y", x, rows, cols, dev)
+    a = OptNorm(rows, cols, _dtype_code(x), wd, x.data_ptr(), ldx, pr, ldr, pw, ph, ldh, py, ldy,
+                _coded(codes, "codes'", rows, cols, dev), float(eps))
+    return _check(lib().opt_rms_norm(ctypes.byref(a), _stream(stream)))
+
+
+def opt_rms_norm_workspace(rows, cols):
+    """Bytes of device workspace opt_rms_norm_backward takes for dweight."""
+    n = lib().opt_rms_norm_workspace(int(rows), int(cols))
+    if n < 0:
+        _check(int(n))
+    return int(n)
+
+
+def _scratch(nbytes, stream):
+    """Device bytes that the allocator hands out again only after `stream`'s
+    work so far: allocated under that stream."""
+    import torch
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream)) if stream else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+
+
+def opt_rms_norm_backward(dy, h, weight, dx, dweight=None, eps=1e-6, dh=None, accumulate=False, workspace=None, stream=None):
+    """Gradients of opt_rms_norm at the h it stored (x without a residual):
+    dx (of x and of the residual) from dy, plus dh where given, and dweight
+    (float32; added to with accumulate).  workspace: a CUDA byte tensor of
+    opt_rms_norm_workspace(rows, cols), or None to take one from torch's
+    allocator."""
+    import torch
+    dev = _device()
+    _on_device(dy, "dy", dev)
+    rows, cols, lddy = _sides(dy, "dy")
+    pw, wd = _weight(weight, cols, dev)
+    ph, ldh = _like(h, "h", dy, rows, cols, dev)
+    pd, lddh = _like(dh, "dh", dy, rows, cols, dev)
+    px, lddx = _like(dx, "dx", dy, rows, cols, dev)
+    need = 0
+    if dweight is not None:
+        _device_buffer(dweight, 4, cols, "dweight")
+        if dweight.dtype != torch.float32:
+            raise ValueError("dweight must be a CUDA float32 tensor")
+        need = opt_rms_norm_workspace(rows, cols)
+        if workspace is None:
+            workspace = _scratch(need, stream)
+        else:
+            _device_buffer(workspace, 1, need, "workspace")
+    a = OptNormGrad(rows, cols, _dtype_code(dy), wd, dy.data_ptr(), lddy, ph, ldh, pw, pd, lddh, px, lddx, _ptr(dweight),
+                    1 if accumulate else 0, 0, float(eps), _ptr(workspace) if need else None, need)
+    return _check(lib().opt_rms_norm_backward(ctypes.byref(a), _stream(stream)))
+
+
+def opt_block_cast(x, codes=None, codes_t=None, block_rows=1, stream=None):
+    """Block-coded E4M3 copies of x [rows, cols]: codes (a pair for rows x
+    cols) and/or codes_t (a pair for the transpose, cols x rows).  block_rows
+    1: a scale for each coded row and 128 of its columns; 128: one for each
+    128 x 128 elements."""
+    dev = _device()
+    _on_device(x, "x", dev)
+    rows, cols, ldx = _sides(x, "x")
+    a = OptCast(rows, cols, x.data_ptr(), ldx, _dtype_code(x), int(block_rows), _coded(codes, "codes'", rows, cols, dev),
+                _coded(codes_t, "codes_t's", cols, rows, dev))
+    return _check(lib().opt_block_cast(ctypes.byref(a), _stream(stream)))
+
+
+def opt_block_matmul(a, b, out, accumulate=False, stream=None):
+    """out [m, n] = a b^T (+ out): a and b block-coded pairs of m and n rows
+    of the same length; out float32, bfloat16 or float16."""
+    dev = _device()
+    _on_device(out, "out", dev)
+    m, n, ldc = _sides(out, "out")
+    k = a[0].shape[1]
+    if b[0].shape[1] != k:
+        raise ValueError(f"a has {k} code columns, b {b[0].shape[1]}")
+    r = OptProduct(m, n, k, _coded(a, "a's", m, k, dev), _coded(b, "b's", n, k, dev), out.data_ptr(), ldc, _dtype_code(out),
+                   1 if accumulate else 0)
+    return _check(lib().opt_block_matmul(ctypes.byref(r), _stream(stream)))
 
 
 def opt_debug_mini(elem, A, x, r, codes, decoded, stream=None):

@@ -17,7 +17,9 @@ LIB = os.path.join(HERE, "libopt_step.so")
 # (source, extra flags): the blockwise step compiles once per parameter storage
 SOURCES = [("opt_api.cpp", []), ("opt_kernels.hip", []), ("opt_kernels_ew.hip", []), ("opt_kernels_1s.hip", []),
            ("opt_kernels_q8.hip", ["-DOPT_Q8_PD=0"]), ("opt_kernels_q8.hip", ["-DOPT_Q8_PD=1"]),
-           ("opt_kernels_q8.hip", ["-DOPT_Q8_PD=2"])]
+           ("opt_kernels_q8.hip", ["-DOPT_Q8_PD=2"]),
+           ("opt_api_pass.cpp", []), ("opt_kernels_drop.hip", []), ("opt_kernels_norm.hip", []),
+           ("opt_kernels_cast.hip", []), ("opt_kernels_mm.hip", [])]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

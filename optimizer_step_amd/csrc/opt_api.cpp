@@ -818,6 +818,20 @@ int check_mini(int32_t elem, float A, const float *x, uint8_t *codes, float *dec
 }
 
 }  // namespace
+
+// The entry points in other files report through the same thread's text.
+int report(int code, const char *fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return fail(code, "%s", buf);
+}
+
+int report_hip(hipError_t e, const char *what) { return hip_fail(e, what); }
+
 }  // namespace optstep
 
 using namespace optstep;

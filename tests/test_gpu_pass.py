@@ -1,0 +1,675 @@
+"""GPU parity of the training-pass operators (dropout, RMS norm, block cast,
+block product) against their plain forms in binary64."""
+import numpy as np
+import pytest
+
+import oracle
+from tests import pass_plain as P
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = ["f32", "bf16", "f16"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    import torch
+    import optimizer_step_amd as osa
+    assert torch.cuda.is_available()
+    osa.lib()
+
+
+def data(seed, rows, cols, dtype, std=1.0):
+    """A host array of the type's values, with rows of different sizes."""
+    rng = np.random.RandomState(seed)
+    return P.rounded(rng.randn(rows, cols) * std * (0.25 + rng.rand(rows, 1)), dtype)
+
+
+def dev(a, dtype, pad=0):
+    """The array on the device, its rows `pad` elements apart from each other."""
+    import torch
+    t = torch.from_numpy(np.ascontiguousarray(a)).to(P.TYPES[dtype])
+    if pad:
+        wide = torch.full((a.shape[0], a.shape[1] + pad), float("nan"), dtype=t.dtype)
+        wide[:, :a.shape[1]] = t
+        return wide.cuda()[:, :a.shape[1]]
+    return t.cuda()
+
+
+def host(t):
+    return t.detach().float().cpu().numpy()
+
+
+def empty(rows, cols, dtype, pad=0):
+    """An output whose surroundings hold a mark."""
+    import torch
+    return torch.full((rows, cols + pad), -77.0, dtype=P.TYPES[dtype], device="cuda")[:, :cols]
+
+
+def untouched(t):
+    """The elements beside a padded output's columns still hold the mark."""
+    base = t._base
+    return base is None or bool((base[:, t.shape[1]:] == -77.0).all())
+
+
+def marked_codes(rows, cols):
+    import torch
+    import optimizer_step_amd as osa
+    q, s = osa.block_buffers(rows + 3, cols)
+    q.fill_(0x5A)
+    s.fill_(0x5A)
+    return q, s
+
+
+def check_coded(pair, codes, scales, rows, cols):
+    """The pair holds exactly these codes and scales, zero padding, and the
+    mark where nothing belongs."""
+    q, s = (t.cpu().numpy() for t in pair)
+    nb = (cols + 127) // 128
+    assert np.array_equal(s[:nb, :rows], scales)
+    assert np.array_equal(q[:rows, :cols], codes)
+    assert not q[:rows, cols:P.up(cols, 16)].any()
+    if q.shape[0] > rows:
+        assert (q[rows:] == 0x5A).all() and (s[:, P.up(rows, 4):] == 0x5A).all()
+
+
+# ---- dropout ----------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [1, 7, 8, 9, 255, 4096, 4099, 20011])
+@pytest.mark.parametrize("res", [False, True])
+def test_dropout(dtype, n, res):
+    import torch
+    import optimizer_step_amd as osa
+    x, r = data(n, 1, n, dtype)[0], data(n + 1, 1, n, dtype)[0] if res else None
+    seed, offset = 0x123456789ABCDEF0 + n, (1 << 40) + n
+    out = torch.full((n + 9,), -77.0, dtype=P.TYPES[dtype], device="cuda")
+    osa.opt_dropout(dev(x, dtype), out[:n], 0.3, seed=seed, offset=offset, residual=dev(r, dtype) if res else None)
+    assert np.array_equal(host(out)[:n], P.rounded(P.dropout(x, r, 0.3, seed, offset), dtype))
+    assert (host(out)[n:] == -77.0).all()
+
+
+@pytest.mark.parametrize("p", [0.0, 1e-6, 1 / 65536, 0.5, 0.999999, 1.0])
+def test_dropout_shares(p):
+    """p at both ends, below a 2^-16 step, and infinities and NaNs under the mask."""
+    import torch
+    import optimizer_step_amd as osa
+    x = data(3, 1, 4096, "f32")[0]
+    bits = P.random_bits(4096, 11, 12)
+    x[bits < p * 65536 - 0.5] = np.nan
+    x[np.argmin(bits)] = np.inf if p > 1e-5 else 1.0
+    out = torch.empty(4096, device="cuda")
+    osa.opt_dropout(dev(x, "f32"), out, p, seed=11, offset=12)
+    want = P.dropout(x, None, p, 11, 12)
+    assert np.array_equal(host(out), want, equal_nan=True)
+    if p == 1.0:
+        assert not host(out).any()
+
+
+def test_dropout_in_place_shards_and_backward():
+    import torch
+    import optimizer_step_amd as osa
+    x, r = data(5, 1, 5000, "bf16")[0], data(6, 1, 5000, "bf16")[0]
+    want = P.rounded(P.dropout(x, r, 0.25, 9, 1), "bf16")
+    a, b = dev(x, "bf16"), dev(r, "bf16")
+    osa.opt_dropout(a, a, 0.25, seed=9, offset=1, residual=b)
+    assert np.array_equal(host(a), want)
+    a = dev(x, "bf16")
+    osa.opt_dropout(a, b, 0.25, seed=9, offset=1, residual=b)
+    assert np.array_equal(host(b), want)
+    parts = torch.empty(5000, dtype=torch.bfloat16, device="cuda")
+    b = dev(r, "bf16")
+    for lo, hi in ((0, 1000), (1000, 1008), (1008, 5000)):
+        osa.opt_dropout(a[lo:hi], parts[lo:hi], 0.25, seed=9, offset=1, residual=b[lo:hi], index_base=lo)
+    assert np.array_equal(host(parts), want)
+    # the gradient passes where the value did, with the same factor
+    g = torch.ones(5000, device="cuda")
+    osa.opt_dropout(g, g, 0.25, seed=9, offset=1)
+    keep = P.random_bits(5000, 9, 1) >= 16384
+    assert np.array_equal(host(g), np.where(keep, np.float32(1 / 0.75), 0))
+
+
+def test_dropout_far_index():
+    """Element indices past 2^35 reach the counter's second word."""
+    import torch
+    import optimizer_step_amd as osa
+    base = (1 << 37) + 8 * 5
+    x = data(5, 1, 64, "f32")[0]
+    out = torch.empty(64, device="cuda")
+    osa.opt_dropout(dev(x, "f32"), out, 0.5, seed=3, offset=4, index_base=base)
+    assert np.array_equal(host(out), P.dropout(x, None, 0.5, 3, 4, base))
+
+
+def test_dropout_unaligned_views():
+    import torch
+    import optimizer_step_amd as osa
+    x = data(8, 1, 1003, "f16")[0]
+    a = torch.zeros(1010, dtype=torch.float16, device="cuda")
+    a[3:1006] = dev(x, "f16")
+    out = torch.full((1010,), -77.0, dtype=torch.float16, device="cuda")
+    osa.opt_dropout(a[3:1006], out[1:1004], 0.4, seed=1, offset=1)
+    assert np.array_equal(host(out[1:1004]), P.rounded(P.dropout(x, None, 0.4, 1, 1), "f16"))
+    assert (host(out)[[0, 1004, 1009]] == -77.0).all()
+
+
+# ---- the norm ---------------------------------------------------------------
+
+NORM_SIZES = [(1, 1), (3, 5), (17, 127), (5, 128), (9, 129), (33, 250), (20, 512), (5, 513), (3, 1000), (2, 2048), (3, 2049),
+              (2, 4099), (3, 8192), (2, 11008), (2, 16385), (1, 32768)]
+
+
+def check_values(got, want, bound):
+    assert np.all(np.abs(got.astype(np.float64) - want) <= bound), np.max(np.abs(got - want) - bound)
+
+
+@pytest.mark.parametrize("rows,cols", NORM_SIZES)
+@pytest.mark.parametrize("dtype,w_dtype", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16"), ("f16", "f16"), ("f32", "bf16")])
+def test_norm(rows, cols, dtype, w_dtype):
+    import torch
+    import optimizer_step_amd as osa
+    x, r = data(cols, rows, cols, dtype), data(cols + 1, rows, cols, dtype)
+    w = P.rounded(0.5 + np.random.RandomState(cols).rand(cols), w_dtype)
+    eps = 1e-5
+    h, y, q = empty(rows, cols, dtype, 3), empty(rows, cols, dtype, 5), marked_codes(rows, cols)
+    osa.opt_rms_norm(dev(x, dtype, 7), dev(w, w_dtype), eps=eps, residual=dev(r, dtype, 1), h=h, y=y, codes=(q[0][:rows], q[1]))
+    want_h = P.rounded(x + r, dtype)
+    assert np.array_equal(host(h), want_h)
+    want = P.norm(want_h, w, eps)
+    check_values(host(y), want, P.norm_bound(want, dtype))
+    assert untouched(h) and untouched(y)
+    # codes: every scale is the rule's for a value within the binary32 bound of
+    # the block's maximum, every code within half a step (of the value's
+    # binade, or the next one's where the binary32 value crosses into it)
+    qh, sh = (t.cpu().numpy() for t in q)
+    nb = (cols + 127) // 128
+    top = P.block_maxima(want, 1).T
+    lo, hi = P.scale_bytes(top * (1 - 4 * P.U32)), P.scale_bytes(top * (1 + 4 * P.U32))
+    s = sh[:nb, :rows]
+    assert np.all((s == lo) | (s == hi))
+    X = np.repeat(2.0 ** (s.T.astype(np.float64) - 127), 128, 1)[:, :cols]
+    got = P.decode(qh[:rows], s, cols)
+    near = np.abs(want) * (1 + 4 * P.U32)
+    step = X * 2.0 ** (np.maximum(np.floor(np.log2(np.maximum(near / X, 2.0 ** -6))), -6) - 3)
+    check_values(got, want, step / 2 + 4 * P.U32 * np.abs(want))
+    assert not qh[:rows, cols:P.up(cols, 16)].any() and (qh[rows:] == 0x5A).all()
+    # without the residual, each output alone gives the same bits from h
+    y2, q2 = empty(rows, cols, dtype), osa.block_buffers(rows, cols)
+    osa.opt_rms_norm(h, dev(w, w_dtype), eps=eps, y=y2)
+    osa.opt_rms_norm(h, dev(w, w_dtype), eps=eps, codes=q2)
+    assert torch.equal(y2, y.contiguous()) and torch.equal(q2[0][:, :cols], q[0][:rows, :cols])
+    assert torch.equal(q2[1][:, :rows], q[1][:, :rows])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_norm_edge_rows(dtype):
+    """Rows of zeros, of one value, with an infinity, with a NaN, tiny and large."""
+    import torch
+    import optimizer_step_amd as osa
+    cols = 300
+    x = np.zeros((7, cols), np.float32)
+    x[1, 7] = 3.0
+    x[2] = 1.0
+    x[2, 200] = np.inf
+    x[3] = 1.0
+    x[3, 100] = np.nan
+    x[4] = P.rounded(np.full(cols, 1e-4), dtype)
+    x[5] = P.rounded(np.full(cols, 6e4), dtype)
+    w = np.ones(cols, np.float32)
+    y, q = empty(7, cols, dtype), osa.block_buffers(7, cols)
+    osa.opt_rms_norm(dev(x, dtype), dev(w, "f32"), eps=1e-6, y=y, codes=q)
+    got = host(y)
+    with np.errstate(invalid="ignore"):
+        want = P.norm(x, w, 1e-6)
+    ok = np.isfinite(want)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.all(np.abs(got[ok] - want[ok]) <= P.norm_bound(want[ok], dtype))
+    assert not got[0].any() and not got[6].any() and not q[0][0].any()
+    s = q[1].cpu().numpy()[:, :7]
+    bad = np.isnan(P.block_maxima(want, 1).T) | np.isinf(P.block_maxima(want, 1).T)
+    assert np.array_equal(s == 255, bad)
+
+
+def test_norm_in_place():
+    import torch
+    import optimizer_step_amd as osa
+    x, r = data(1, 6, 1000, "bf16"), data(2, 6, 1000, "bf16")
+    w = dev(np.ones(1000, np.float32), "bf16")
+    h, y = empty(6, 1000, "bf16"), empty(6, 1000, "bf16")
+    osa.opt_rms_norm(dev(x, "bf16"), w, residual=dev(r, "bf16"), h=h, y=y)
+    a, b = dev(x, "bf16"), dev(r, "bf16")
+    osa.opt_rms_norm(a, w, residual=b, h=b, y=a)
+    assert torch.equal(b, h) and torch.equal(a, y)
+
+
+@pytest.mark.parametrize("rows,cols", NORM_SIZES + [(1500, 128), (2100, 1000), (1100, 2049)])
+@pytest.mark.parametrize("dtype,w_dtype", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16"), ("f16", "f16")])
+@pytest.mark.parametrize("more", [False, True])
+def test_norm_backward(rows, cols, dtype, w_dtype, more):
+    import torch
+    import optimizer_step_amd as osa
+    dy, h = data(cols, rows, cols, dtype, 0.1), data(cols + 1, rows, cols, dtype)
+    w = P.rounded(0.5 + np.random.RandomState(cols).rand(cols), w_dtype)
+    dh = data(cols + 2, rows, cols, dtype, 0.1) if more else None
+    eps = 1e-5
+    dx = empty(rows, cols, dtype, 3)
+    start = np.random.RandomState(cols).randn(cols).astype(np.float32) if more else np.zeros(cols, np.float32)
+    dw = torch.from_numpy(start.copy()).cuda() if more else torch.full((cols,), -5.0, device="cuda")
+    osa.opt_rms_norm_backward(dev(dy, dtype, 1), dev(h, dtype, 2), dev(w, w_dtype), dx, dw, eps=eps,
+                              dh=dev(dh, dtype, 8) if more else None, accumulate=more)
+    want, want_w, size, size_w = P.norm_gradients(dy, h, w, dh, eps)
+    # seven roundings at most touch a term before the last sum's and the store's
+    check_values(host(dx), want, 9 * P.U32 * size + P.HALF[dtype] * (1 + 16 * P.U32) * np.abs(want) + 9 * P.U32 * P.HALF[dtype] * size
+                 + P.TINY[dtype])
+    assert untouched(dx)
+    # three roundings a term, binary32 sums of at most `run` terms, binary64 after
+    run = rows / max(1, osa.opt_rms_norm_workspace(rows, cols) // (4 * cols)) + 8
+    check_values(dw.cpu().numpy(), want_w + start, (3 + run) * P.U32 * size_w + 2 * P.U32 * np.abs(want_w + start))
+    # dx alone
+    dx2 = empty(rows, cols, dtype)
+    osa.opt_rms_norm_backward(dev(dy, dtype), dev(h, dtype), dev(w, w_dtype), dx2, eps=eps, dh=dev(dh, dtype) if more else None)
+    assert torch.equal(dx2, dx.contiguous())
+
+
+def test_norm_backward_no_rows():
+    import torch
+    import optimizer_step_amd as osa
+    e = torch.empty(0, 64, device="cuda")
+    w, dw = torch.ones(64, device="cuda"), torch.full((64,), 3.0, device="cuda")
+    osa.opt_rms_norm_backward(e, e, w, e, dw, accumulate=True)
+    assert (host(dw) == 3.0).all()
+    osa.opt_rms_norm_backward(e, e, w, e, dw)
+    assert not host(dw).any()
+
+
+def test_norm_backward_in_place():
+    import torch
+    import optimizer_step_amd as osa
+    dy, h, dh = data(1, 40, 500, "bf16"), data(2, 40, 500, "bf16"), data(3, 40, 500, "bf16")
+    w = dev(np.ones(500, np.float32), "f32")
+    dx, dw, dw2 = empty(40, 500, "bf16"), torch.empty(500, device="cuda"), torch.empty(500, device="cuda")
+    osa.opt_rms_norm_backward(dev(dy, "bf16"), dev(h, "bf16"), w, dx, dw, dh=dev(dh, "bf16"))
+    for which in (0, 1):
+        a = [dev(dy, "bf16"), dev(dh, "bf16")]
+        osa.opt_rms_norm_backward(a[0], dev(h, "bf16"), w, a[which], dw2, dh=a[1])
+        assert torch.equal(a[which], dx) and torch.equal(dw, dw2)
+
+
+# ---- the cast ---------------------------------------------------------------
+
+CAST_SIZES = [(1, 1), (1, 128), (3, 16), (5, 130), (128, 128), (127, 255), (129, 257), (130, 17), (300, 511), (260, 1000)]
+
+
+def cast_input(rows, cols, dtype):
+    x = data(rows * 1000 + cols, rows, cols, dtype)
+    if x.size > 100:
+        x[0, :] *= 0                                            # a block row of zeros, -0 among them
+        x[0, 1::2] = -0.0
+        x[-1, -1] = 448.0                                       # the grid's end, and just past it
+        x[rows // 2, 0] = P.rounded(np.array([450.0]), dtype)[0]
+        x[min(1, rows - 1), cols // 2] = P.rounded(np.array([1e-6]), dtype)[0]
+    return x
+
+
+@pytest.mark.parametrize("rows,cols", CAST_SIZES)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_cast(rows, cols, dtype, block_rows):
+    import torch
+    import optimizer_step_amd as osa
+    x = cast_input(rows, cols, dtype)
+    q, qt = marked_codes(rows, cols), marked_codes(cols, rows)
+    osa.opt_block_cast(dev(x, dtype, 3), codes=(q[0][:rows], q[1]), codes_t=(qt[0][:cols], qt[1]), block_rows=block_rows)
+    check_coded(q, *P.encode(x, block_rows), rows, cols)
+    check_coded(qt, *P.encode(x.T.copy(), block_rows), cols, rows)
+    for which in (0, 1):
+        sides = (rows, cols) if which == 0 else (cols, rows)
+        one = osa.block_buffers(*sides)
+        osa.opt_block_cast(dev(x, dtype), block_rows=block_rows, **{("codes", "codes_t")[which]: one})
+        both = (q, qt)[which]
+        assert torch.equal(one[0], both[0][:sides[0]]) and torch.equal(one[1][:, :sides[0]], both[1][:one[1].shape[0], :sides[0]])
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_cast_range(block_rows):
+    """Blocks over the whole binary32 range, subnormals, infinities and NaNs."""
+    import optimizer_step_amd as osa
+    rng = np.random.RandomState(4)
+    rows = 300
+    x = (rng.randn(rows, 256) * 2.0 ** np.linspace(-146, 126, rows)[:, None]).astype(np.float32)
+    x[10, 3], x[200, 130], x[290, 255] = np.inf, np.nan, -np.inf
+    q, qt = osa.block_buffers(rows, 256), osa.block_buffers(256, rows)
+    osa.opt_block_cast(dev(x, "f32"), codes=q, codes_t=qt, block_rows=block_rows)
+    for pair, v in ((q, x), (qt, x.T.copy())):
+        codes, scales = P.encode(v, block_rows)
+        assert np.array_equal(pair[1].cpu().numpy()[:, :v.shape[0]], scales)
+        assert np.array_equal(pair[0].cpu().numpy(), np.pad(codes, ((0, 0), (0, pair[0].shape[1] - v.shape[1]))))
+
+
+def test_cast_every_value():
+    """Every BF16 word as its own block's second value beside a fixed maximum."""
+    import torch
+    import optimizer_step_amd as osa
+    words = np.arange(65536, dtype=np.uint16)
+    v = oracle.widen_bf16(words)
+    v = v[np.isfinite(v) & (np.abs(v) <= 448)]
+    x = np.zeros((v.size, 2), np.float32)
+    x[:, 0], x[:, 1] = 448.0, v
+    q = osa.block_buffers(v.size, 2)
+    osa.opt_block_cast(dev(x, "bf16"), codes=q)
+    assert np.array_equal(q[0].cpu().numpy()[:, :2], P.encode(x)[0])
+
+
+def test_cast_offsets_past_32_bits():
+    """Rows more than 2^32 elements apart."""
+    import torch
+    import optimizer_step_amd as osa
+    ld, rows = (1 << 21) + 24, 2100
+    big = torch.empty(rows * ld, dtype=torch.bfloat16, device="cuda").view(rows, ld)
+    x = data(9, rows, 40, "bf16")
+    big[:, 8:48] = dev(x, "bf16")
+    q, qt = osa.block_buffers(rows, 40), osa.block_buffers(40, rows)
+    osa.opt_block_cast(big[:, 8:48], codes=q, codes_t=qt)
+    check_coded(q, *P.encode(x), rows, 40)
+    check_coded(qt, *P.encode(x.T.copy()), 40, rows)
+    y = empty(rows, 40, "bf16")
+    w = torch.ones(40, device="cuda")
+    osa.opt_rms_norm(big[:, 8:48], w, y=y)
+    want = P.norm(x, np.ones(40), 1e-6)
+    check_values(host(y), want, P.norm_bound(want, "bf16"))
+
+
+# ---- the product ------------------------------------------------------------
+
+
+def coded(seed, rows, k, whole):
+    """A random block-coded matrix: (pair on the device, its values [rows, k]).
+    `whole`: small whole values and scales of 1 to 4, so that every partial sum
+    of a product is exact in binary32 whatever its order."""
+    import torch
+    import optimizer_step_amd as osa
+    rng = np.random.RandomState(seed)
+    pair = osa.block_buffers(rows, k)
+    nb = (k + 127) // 128
+    if whole:
+        table = np.array([P.nearest_code(np.array([float(v)]))[0] for v in range(9)], np.uint8)
+        codes = table[rng.randint(0, 9, (rows, k))] | (rng.randint(0, 2, (rows, k)) * 0x80).astype(np.uint8)
+        scales = rng.randint(127, 130, (nb, rows)).astype(np.uint8)
+    else:
+        codes = rng.randint(0, 127, (rows, k)).astype(np.uint8) | (rng.randint(0, 2, (rows, k)) * 0x80).astype(np.uint8)
+        scales = rng.randint(110, 140, (nb, rows)).astype(np.uint8)
+    pair[0][:, :k] = torch.from_numpy(codes).cuda()
+    pair[1].fill_(255)                                  # the scales past the last row say NaN: no row is theirs
+    pair[1][:, :rows] = torch.from_numpy(scales).cuda()
+    return pair, P.decode(codes, scales, k)
+
+
+MM_SIZES = [(1, 1, 1), (1, 16, 16), (1, 300, 128), (2, 17, 129), (3, 64, 1000), (5, 1000, 511), (16, 16, 256), (17, 33, 640),
+            (31, 129, 1040), (33, 200, 130), (64, 128, 512), (65, 300, 384), (100, 257, 2050), (128, 128, 128), (129, 130, 131),
+            (130, 515, 300), (256, 256, 1024), (257, 255, 4100), (300, 700, 96), (513, 260, 1552), (1025, 129, 272), (70, 2100, 600)]
+
+
+@pytest.mark.parametrize("m,n,k", MM_SIZES)
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_product_whole(m, n, k, dtype):
+    """Whole values: every sum is exact, so the result is the exact one rounded once."""
+    import optimizer_step_amd as osa
+    a, av = coded(m + k, m, k, True)
+    b, bv = coded(n + k, n, k, True)
+    c = empty(m, n, dtype, 5)
+    osa.opt_block_matmul(a, b, c)
+    want = av @ bv.T
+    assert np.abs(want).max() < 2 ** 24 * 16 and untouched(c)
+    assert np.array_equal(host(c), P.rounded(want, dtype))
+    c2 = empty(m, n, dtype, 5)
+    c2.fill_(3.0)
+    osa.opt_block_matmul(a, b, c2, accumulate=True)
+    assert np.array_equal(host(c2), P.rounded(want + 3.0, dtype)) and untouched(c2)
+
+
+@pytest.mark.parametrize("m,n,k", MM_SIZES)
+def test_product_random(m, n, k):
+    """Any codes and scales: within the bound of a binary32 sum in any order,
+    each addition off by at most a step (2^-23) of the running magnitude."""
+    import optimizer_step_amd as osa
+    a, av = coded(m + k, m, k, False)
+    b, bv = coded(n + k, n, k, False)
+    c = empty(m, n, "f32")
+    osa.opt_block_matmul(a, b, c)
+    check_values(host(c), av @ bv.T, (k + 8) * 2.0 ** -23 * (np.abs(av) @ np.abs(bv).T))
+
+
+def test_product_nan_rows_and_scales():
+    """A block whose scale says NaN, and NaN codes, poison their own rows and
+    columns and nothing else."""
+    import optimizer_step_amd as osa
+    for m, n, k in ((5, 40, 300), (200, 300, 300), (300, 600, 640)):
+        a, av = coded(1, m, k, True)
+        b, bv = coded(2, n, k, True)
+        a[1][1, 3] = 255
+        b[0][n - 1, 7] = 0x7F
+        c = empty(m, n, "bf16")
+        osa.opt_block_matmul(a, b, c)
+        want = P.rounded(av @ bv.T, "bf16")
+        want[3, :] = np.nan
+        want[:, n - 1] = np.nan
+        assert np.array_equal(host(c), want, equal_nan=True)
+
+
+def test_product_slices_and_strides():
+    """Row and column slices of larger coded matrices, a padded output."""
+    import optimizer_step_amd as osa
+    a, av = coded(1, 100, 640, True)
+    b, bv = coded(2, 90, 640, True)
+    c = empty(40, 50, "f32", 7)
+    osa.opt_block_matmul((a[0][8:48, 128:512], a[1][1:4, 8:48]), (b[0][4:54, 128:512], b[1][1:4, 4:56]), c)
+    assert np.array_equal(host(c), (av[8:48, 128:512] @ bv[4:54, 128:512].T).astype(np.float32)) and untouched(c)
+
+
+def test_product_no_columns():
+    import torch
+    import optimizer_step_amd as osa
+    a, b = osa.block_buffers(3, 0), osa.block_buffers(5, 0)
+    c = torch.full((3, 5), 2.0, device="cuda")
+    osa.opt_block_matmul(a, b, c, accumulate=True)
+    assert (host(c) == 2.0).all()
+    osa.opt_block_matmul(a, b, c)
+    assert not host(c).any()
+
+
+# ---- the binding's refusals, streams, graphs --------------------------------
+
+
+def test_binding_refusals():
+    import torch
+    import optimizer_step_amd as osa
+    x, w, y = (torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in ((4, 128), (128,), (4, 128)))
+    q = osa.block_buffers(4, 128)
+    for call in (
+        lambda: osa.opt_dropout(x.t(), y, 0.1),
+        lambda: osa.opt_dropout(x, y.float(), 0.1),
+        lambda: osa.opt_dropout(x, y[:2], 0.1),
+        lambda: osa.opt_rms_norm(x, w[:5], y=y),
+        lambda: osa.opt_rms_norm(x.t(), w, y=y),
+        lambda: osa.opt_rms_norm(x, w, y=y.float()),
+        lambda: osa.opt_rms_norm(x, w, codes=osa.block_buffers(3, 128)),
+        lambda: osa.opt_rms_norm(x, w, codes=osa.block_buffers(4, 96)),
+        lambda: osa.opt_rms_norm_backward(x, y, w, x.clone(), torch.zeros(128, dtype=torch.float64, device="cuda")),
+        lambda: osa.opt_rms_norm_backward(x, y, w, x.clone(), torch.zeros(128, device="cuda"),
+                                          workspace=torch.zeros(8, dtype=torch.uint8, device="cuda")),
+        lambda: osa.opt_block_cast(x, codes=osa.block_buffers(128, 4)),
+        lambda: osa.opt_block_matmul(q, osa.block_buffers(4, 256), torch.zeros(4, 4, device="cuda")),
+        lambda: osa.opt_block_matmul(q, q, torch.zeros(4, 5, device="cuda")),
+        lambda: osa.opt_block_matmul((q[0], q[1][:, :3]), q, torch.zeros(4, 4, device="cuda")),
+    ):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: osa.opt_rms_norm(x, w), lambda: osa.opt_dropout(x, y, 2.0), lambda: osa.opt_block_cast(x, codes=q, block_rows=3),
+                 lambda: osa.opt_rms_norm(x[:1].expand(4, 128), w, y=y)):
+        with pytest.raises(osa.OptError):
+            call()
+
+
+def layer(osa, t, stream=None):
+    """One layer's pass, forward and backward, over preallocated tensors."""
+    kw = dict(stream=stream)
+    osa.opt_dropout(t["x"], t["d"], 0.2, seed=5, offset=6, residual=t["res"], **kw)
+    osa.opt_rms_norm(t["d"], t["w"], y=t["y"], codes=t["yq"], **kw)
+    osa.opt_block_cast(t["W"], codes=t["Wq"], codes_t=t["Wt"], block_rows=128, **kw)
+    osa.opt_block_matmul(t["yq"], t["Wq"], t["z"], **kw)
+    osa.opt_block_cast(t["y"], codes_t=t["yt"], **kw)
+    osa.opt_block_cast(t["dz"], codes=t["dzq"], codes_t=t["dzt"], **kw)
+    osa.opt_block_matmul(t["dzq"], t["Wt"], t["dy"], **kw)
+    osa.opt_block_matmul(t["dzt"], t["yt"], t["dW"], **kw)
+    osa.opt_rms_norm_backward(t["dy"], t["d"], t["w"], t["dd"], t["dw"], **kw)
+    osa.opt_dropout(t["dd"], t["dx"], 0.2, seed=5, offset=6, **kw)
+
+
+def layer_tensors(osa, tokens, inner, outer, seed=1):
+    import torch
+    t = {"x": dev(data(seed, tokens, inner, "bf16"), "bf16"), "res": dev(data(seed + 1, tokens, inner, "bf16"), "bf16"),
+         "w": dev(1 + 0.1 * data(seed + 2, 1, inner, "f32")[0], "f32"), "W": dev(data(seed + 3, outer, inner, "f32", 0.05), "f32"),
+         "dz": dev(data(seed + 4, tokens, outer, "bf16", 0.01), "bf16")}
+    for name, shape, dt in (("d", (tokens, inner), "bf16"), ("y", (tokens, inner), "bf16"), ("z", (tokens, outer), "bf16"),
+                            ("dy", (tokens, inner), "bf16"), ("dd", (tokens, inner), "bf16"), ("dx", (tokens, inner), "bf16"),
+                            ("dW", (outer, inner), "f32"), ("dw", (inner,), "f32")):
+        t[name] = torch.zeros(shape, dtype=P.TYPES[dt], device="cuda")
+    for name, rows, cols in (("yq", tokens, inner), ("Wq", outer, inner), ("Wt", inner, outer), ("yt", inner, tokens),
+                             ("dzq", tokens, outer), ("dzt", outer, tokens)):
+        t[name] = osa.block_buffers(rows, cols)
+    return t
+
+
+OUTPUTS = ("d", "y", "z", "dy", "dd", "dx", "dW", "dw")
+
+
+@pytest.mark.parametrize("tokens,inner,outer", [(1, 256, 96), (77, 300, 517), (512, 640, 384)])
+def test_layer_then_step(tokens, inner, outer):
+    """The pass as a program runs it, each operator against its plain form on
+    what the one before it wrote, then clipping and the step on its gradients."""
+    import torch
+    import optimizer_step_amd as osa
+    t = layer_tensors(osa, tokens, inner, outer)
+    layer(osa, t)
+    H = {k: host(v) for k, v in t.items() if torch.is_tensor(v)}
+    C = {k: (v[0].cpu().numpy(), v[1].cpu().numpy()) for k, v in t.items() if not torch.is_tensor(v)}
+    val = lambda k, rows, cols: P.decode(C[k][0], C[k][1][:, :rows], cols)  # noqa: E731
+    assert np.array_equal(H["d"], P.rounded(P.dropout(H["x"], H["res"], 0.2, 5, 6), "bf16"))
+    want = P.norm(H["d"], H["w"], 1e-6)
+    check_values(H["y"], want, P.norm_bound(want, "bf16"))
+    for name, x, rows in (("Wq", H["W"], 128), ("Wt", H["W"].T.copy(), 128), ("yt", H["y"].T.copy(), 1), ("dzq", H["dz"], 1),
+                          ("dzt", H["dz"].T.copy(), 1)):
+        codes, scales = P.encode(x, rows)
+        assert np.array_equal(C[name][0][:, :x.shape[1]], codes) and np.array_equal(C[name][1][:, :x.shape[0]], scales)
+    for out, a, b, m, n, k, dt in (("z", "yq", "Wq", tokens, outer, inner, "bf16"), ("dy", "dzq", "Wt", tokens, inner, outer, "bf16"),
+                                   ("dW", "dzt", "yt", outer, inner, tokens, "f32")):
+        av, bv = val(a, m, k), val(b, n, k)
+        want, size = av @ bv.T, np.abs(av) @ np.abs(bv).T
+        check_values(H[out], want, P.HALF[dt] * np.abs(want) * 1.001 + (k + 8) * 2.0 ** -23 * size + P.TINY[dt])
+    want, want_w, size, size_w = P.norm_gradients(H["dy"], H["d"], H["w"], None, 1e-6)
+    check_values(H["dd"], want, 10 * P.U32 * size + P.HALF["bf16"] * 1.001 * np.abs(want) + P.TINY["bf16"])
+    check_values(H["dw"], want_w, 16 * P.U32 * size_w + 2 * P.U32 * np.abs(want_w))
+    assert np.array_equal(H["dx"], P.rounded(P.dropout(H["dd"], None, 0.2, 5, 6), "bf16"))
+    # the gradients go where the step reads them
+    grads = [t["dW"].view(-1), t["dw"]]
+    norms = torch.empty(6, dtype=torch.float64, device="cuda")
+    coef = torch.empty(1, device="cuda")
+    osa.opt_grad_norm(grads, norms, max_norm=0.5, coef_out=coef)
+    steps = [dict(p=t["W"].view(-1), g=grads[0], **osa.state_buffers("f32", outer * inner)),
+             dict(p=t["w"], g=grads[1], **osa.state_buffers("f32", inner))]
+    osa.opt_step_adamw(steps, "f32", osa.hparams(lr=1e-2, weight_decay=0.1, step=1, grad_scale=coef))
+    from tests.gpu_common import fp32_close
+    for d, p, g in ((steps[0], H["W"].reshape(-1), H["dW"].reshape(-1)), (steps[1], H["w"], H["dw"])):
+        st = oracle.state_zeros("f32", p.size)
+        p = p.copy()
+        oracle.step("adamw", "f32", oracle.make_hp(lr=1e-2, weight_decay=0.1, step=1), p,
+                    (g * np.float32(coef.item())).astype(np.float32), **st)
+        assert fp32_close(host(d["p"]), p)
+
+
+def test_layer_on_another_stream():
+    import torch
+    import optimizer_step_amd as osa
+    a, b = layer_tensors(osa, 200, 384, 256), layer_tensors(osa, 200, 384, 256)
+    layer(osa, a)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        for k in OUTPUTS:
+            b[k].zero_()
+        torch.cuda.synchronize()
+        layer(osa, b, stream)
+        s.synchronize()
+        assert all(torch.equal(a[k], b[k]) for k in OUTPUTS)
+
+
+def test_two_streams_at_once():
+    import torch
+    import optimizer_step_amd as osa
+    want = [layer_tensors(osa, 300, 512, 256, seed) for seed in (1, 50)]
+    got = [layer_tensors(osa, 300, 512, 256, seed) for seed in (1, 50)]
+    for t in want:
+        layer(osa, t)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for t, s in zip(got, streams):
+            layer(osa, t, s)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(a[k], b[k]) for k in OUTPUTS)
+
+
+def test_captured_layers():
+    """Two captured passes, replayed in turn with eager work between, give the
+    eager bits every time."""
+    import torch
+    import optimizer_step_amd as osa
+    want = [layer_tensors(osa, 130, 384, 256, seed) for seed in (1, 50)]
+    got = [layer_tensors(osa, 130, 384, 256, seed) for seed in (1, 50)]
+    for t in want:
+        layer(osa, t)
+    torch.cuda.synchronize()
+    graphs = []
+    for t in got:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            layer(osa, t)
+        graphs.append(g)
+    other = layer_tensors(osa, 64, 256, 128, 9)
+    for _ in range(3):
+        for t in got:
+            for k in OUTPUTS:
+                t[k].zero_()
+        graphs[0].replay()
+        graphs[1].replay()
+        layer(osa, other)
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(a[k], b[k]) for k in OUTPUTS)
+    # two replays of the passes that overlap on two streams: each has its own workspace
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s, g in zip(streams, graphs):
+        with torch.cuda.stream(s):
+            g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(a[k], b[k]) for k in OUTPUTS)
+
+
+def test_product_small_scales():
+    """The smallest scale, on a block of tiny values against large ones."""
+    import torch
+    import optimizer_step_amd as osa
+    a, b = osa.block_buffers(4, 256), osa.block_buffers(16, 256)
+    x = np.ones((4, 256), np.float32)
+    x[:, :128] = 1.5 * 2.0 ** -119
+    osa.opt_block_cast(dev(x, "f32"), codes=a)
+    osa.opt_block_cast(torch.full((16, 256), 2.0 ** 100, device="cuda"), codes=b)
+    assert int(a[1][0, 0]) == 0
+    c = empty(4, 16, "f32")
+    osa.opt_block_matmul(a, b, c)
+    want = 128 * 2.0 ** 100 * (1 + 1.5 * 2.0 ** -119)
+    assert np.array_equal(host(c), np.full((4, 16), want, np.float32))
+    osa.opt_block_matmul((a[0][:, :128], a[1]), (b[0][:, :128], b[1]), c)
+    assert np.array_equal(host(c), np.full((4, 16), 1.5 * 128 * 2.0 ** -19, np.float32))
