@@ -108,9 +108,269 @@ __global__ __launch_bounds__(256) void product_rows_kernel(MatmulArgs a)
     }
 }
 
+// ---------------------------------------------------------------------------
+// Tiles of C through LDS, for products of many rows.
+
+typedef int i8v __attribute__((ext_vector_type(8)));
+typedef float f16v __attribute__((ext_vector_type(16)));
+
+constexpr int kStage = 128;        // columns (code bytes) of a stage: one scale block
+constexpr int64_t kTileMaxLd = (int64_t)1 << 23;   // keeps a tile's row offsets below 2^31
+
+#define OPT_LDS __attribute__((address_space(3)))
+
+// A workgroup of WM x WN waves forms (32 TM WM) x (32 TN WN) of C; a wave,
+// TM x TN tiles of 32 x 32.  A stage is 128 bytes of each of its rows of A and
+// B, copied from global memory into LDS with no register between (16 bytes a
+// lane); two stages are held.  While the matrix cores work on one half of a
+// stage, the other half's codes move from LDS to registers:
+//
+//   read half 1 of s, multiply half 0 of s | barrier | copy stage s + 2 to
+//   where s was, read half 0 of s + 1, multiply half 1 of s | ...
+//
+// Tile i of a wave's T tiles takes its rows T r + i (r = lane % 32), so that
+// the scales of a lane's rows in all its tiles are neighbouring bytes: one
+// load brings them.  16-byte piece c of row R sits at c ^ ((R / T) % 8): the
+// reads of eight neighbouring lanes then fall into different banks.
+template <int ROWS, int T, int THREADS>
+struct StageCopy {
+    static constexpr int kCopies = ROWS * 8 / THREADS;     // 16-byte pieces a thread copies
+    int off[kCopies];
+
+    __device__ __forceinline__ void init(int64_t row0, int64_t rows, int64_t ld)
+    {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const int slot = i * THREADS + threadIdx.x, r = slot >> 3;
+            const int row = (int)min((int64_t)r, rows - 1 - row0);      // rows past the last repeat it; they are not stored
+            off[i] = row * (int)ld + 16 * ((slot & 7) ^ ((r / T) & 7));
+        }
+    }
+    // p: the tile's first row
+    __device__ __forceinline__ void copy(const uint8_t *p, int k0, uint8_t *lds) const
+    {
+        const auto src = __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, 0x7FFFFFFF, 0x00027000);
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (OPT_LDS void *)(lds + 16 * (i * THREADS + (threadIdx.x & ~63))), 16,
+                                                     off[i], k0, 0, 0);
+    }
+    // the last stage of rows that end inside it: pieces past the end are zeros
+    __device__ __forceinline__ void copy_tail(const uint8_t *p, uint8_t *lds, int left) const
+    {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const int slot = i * THREADS + threadIdx.x, c = 16 * ((slot & 7) ^ ((slot >> 3) / T & 7));
+            u4 v = {0, 0, 0, 0};
+            if (c < left) v = gld<u4>(p + off[i]);
+            *(u4 *)(lds + 16 * slot) = v;
+        }
+    }
+};
+
+// The T scale bytes of rows T r .. T r + T - 1 of a wave's rows.
+template <int T>
+__device__ __forceinline__ uint32_t row_scales(const Codes &q, int64_t block, int64_t row, int64_t rows)
+{
+    const int64_t at = min(row, ((rows + 3) & ~(int64_t)3) - 4 + (T == 4 ? 0 : 2));
+    const uint8_t *p = q.scales + block * q.lds + at;
+    return T == 4 ? gld<uint32_t>(p) : (uint32_t)gld<uint16_t>(p);
+}
+
+// Where a lane's 32 bytes of either half (64 columns) of its row of tile 0 sit
+// in a stage; tile i's are i rows on, a constant the read instruction holds.
+struct LaneRow {
+    int piece[2][2];
+
+    // first: the wave's first row, a multiple of 8 T
+    template <int T>
+    __device__ __forceinline__ void init(int first)
+    {
+        const int r = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                int o = (first + T * r) * kStage + 16 * ((4 * half + 2 * h + b) ^ (r & 7));
+                asm("" : "+v"(o));          // one register: not formed again from its parts for every tile
+                piece[half][b] = o;
+            }
+    }
+    __device__ __forceinline__ i8v read(const uint8_t *lds, int i, int half) const
+    {
+        const u4 lo = *(const u4 *)(lds + piece[half][0] + i * kStage);
+        const u4 hi = *(const u4 *)(lds + piece[half][1] + i * kStage);
+        return (i8v){(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+    }
+};
+
+__device__ __forceinline__ f16v mfma_codes(const i8v &b, int sb, const i8v &a, int sa, const f16v &c)
+{
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 0, 0, 0, sb, 0, sa);
+}
+
+// One tile row of a half: acc[j] += fb[j] x fa.
+template <bool EXACT, int TN>
+__device__ __forceinline__ void multiply(f16v (&acc)[TN], const i8v &fa, const i8v (&fb)[TN], uint32_t sa, uint32_t sb)
+{
+    if (!EXACT) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            acc[j] = mfma_codes(fb[j], (int)(sb >> (8 * j)), fa, (int)sa, acc[j]);
+    } else {
+        const float ma = scale_of(sa & 255u);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const bf8v wa = widen8((uint32_t)fa[2 * s], (uint32_t)fa[2 * s + 1], ma);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const bf8v wb = widen8((uint32_t)fb[j][2 * s], (uint32_t)fb[j][2 * s + 1], scale_of((sb >> (8 * j)) & 255u));
+                acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb, wa, acc[j], 0, 0, 0);
+            }
+        }
+    }
+}
+
+// Every wave's copies into LDS and reads from it have ended.
+__device__ __forceinline__ void stage_barrier()
+{
+    __builtin_amdgcn_s_waitcnt(0x0070);     // vmcnt(0) lgkmcnt(0)
+    __syncthreads();
+}
+
+#define SCHED() __builtin_amdgcn_sched_barrier(0)
+
+template <int DT, bool EXACT, int WM, int WN, int TM, int TN>
+__global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(MatmulArgs a)
+{
+#if defined(__HIP_DEVICE_COMPILE__)   // the host pass has no buffer and matrix builtins, and needs the name alone
+    constexpr int kThr = 64 * WM * WN, BM = 32 * TM * WM, BN = 32 * TN * WN;
+    __shared__ __attribute__((aligned(16))) uint8_t la0[BM * kStage], la1[BM * kStage], lb0[BN * kStage], lb1[BN * kStage];
+    const int wave = threadIdx.x >> 6, r = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
+    const int wm = (wave / WN) * 32 * TM, wn = (wave % WN) * 32 * TN;
+    const int64_t tm = (a.m + BM - 1) / BM, tn = (a.n + BN - 1) / BN;
+    const int64_t t = blockIdx.x;
+    const int64_t m0 = (t / tn) * BM, n0 = (t % tn) * BN;
+    (void)tm;
+    StageCopy<BM, TM, kThr> ca;
+    StageCopy<BN, TN, kThr> cb;
+    const uint8_t *pa = a.a.codes + m0 * a.a.ld, *pb = a.b.codes + n0 * a.b.ld;
+    ca.init(m0, a.m, a.a.ld);
+    cb.init(n0, a.n, a.b.ld);
+    const int64_t ra = m0 + wm + TM * r, rb = n0 + wn + TN * r;
+    const int stages = (int)(a.k / kStage), last = stages - 1;
+    f16v acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+    LaneRow la_row, lb_row;
+    la_row.init<TM>(wm);
+    lb_row.init<TN>(wn);
+    i8v fa[TM], fb0[TN], fb1[TN];
+    uint32_t sa, sb;
+    // One half: tile row i is multiplied, then the registers of its codes take
+    // the next half's.
+    auto half_step = [&](const i8v (&fb)[TN], i8v (&nb)[TN], const uint8_t *la, const uint8_t *lb, int half) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) nb[j] = lb_row.read(lb, j, half);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            SCHED();
+            multiply<EXACT, TN>(acc[i], fa[i], fb, sa >> (8 * i), sb);
+            fa[i] = la_row.read(la, i, half);
+        }
+        SCHED();
+    };
+    // stage s is in (la, lb), its half 0 in registers; past the last stage it
+    // copies and reads that one again, which nothing uses
+    auto stage = [&](int s, uint8_t *la, uint8_t *lb, uint8_t *na, uint8_t *nb) {
+        const uint32_t ta = row_scales<TM>(a.a, min(s + 1, last), ra, a.m), tb = row_scales<TN>(a.b, min(s + 1, last), rb, a.n);
+        half_step(fb0, fb1, la, lb, 1);
+        stage_barrier();               // everyone's reads of this stage and copies of the next have ended
+        ca.copy(pa, min(s + 2, last) * kStage, la);
+        cb.copy(pb, min(s + 2, last) * kStage, lb);
+        half_step(fb1, fb0, na, nb, 0);
+        sa = ta;
+        sb = tb;
+    };
+    ca.copy(pa, 0, la0);
+    cb.copy(pb, 0, lb0);
+    stage_barrier();
+    ca.copy(pa, min(1, last) * kStage, la1);
+    cb.copy(pb, min(1, last) * kStage, lb1);
+    sa = row_scales<TM>(a.a, 0, ra, a.m);
+    sb = row_scales<TN>(a.b, 0, rb, a.n);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) fa[i] = la_row.read(la0, i, 0);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) fb0[j] = lb_row.read(lb0, j, 0);
+    int s = 0;
+    for (; s + 1 < stages; s += 2) {
+        stage(s, la0, lb0, la1, lb1);
+        stage(s + 1, la1, lb1, la0, lb0);
+    }
+    if (s < stages) stage(s, la0, lb0, la1, lb1);
+    if (a.k % kStage) {
+        const int64_t k0 = (int64_t)stages * kStage;
+        stage_barrier();
+        ca.copy_tail(pa + k0, la0, (int)(a.k - k0));
+        cb.copy_tail(pb + k0, lb0, (int)(a.k - k0));
+        sa = row_scales<TM>(a.a, stages, ra, a.m);
+        sb = row_scales<TN>(a.b, stages, rb, a.n);
+        stage_barrier();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) fb0[j] = lb_row.read(lb0, j, half);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) multiply<EXACT, TN>(acc[i], la_row.read(la0, i, half), fb0, sa >> (8 * i), sb);
+        }
+    }
+    // lane (r, h) holds rows TM r + i of C and, of the columns TN x + j, those
+    // with x = 8 g + 4 h + e: 4 TN neighbouring ones for each g
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int64_t m = ra + i;
+        if (m >= a.m) break;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int64_t n = n0 + wn + TN * (8 * g + 4 * h);
+            float v[4 * TN];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) v[TN * e + j] = acc[i][j][4 * g + e];
+#pragma unroll
+            for (int p = 0; p < TN / 2; ++p) {
+                const int cnt = left8(n + 8 * p, a.n);
+                if (a.accumulate) {
+                    float old[8];
+                    load8<DT>(a.c, m * a.ldc + n + 8 * p, cnt, old);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[8 * p + e] = old[e] + v[8 * p + e];
+                }
+                store8<DT>(a.c, m * a.ldc + n + 8 * p, cnt, v + 8 * p);
+            }
+        }
+    }
+#endif
+}
+
 template <int DT>
 static hipError_t launch_matmul_t(const MatmulArgs &a, hipStream_t st)
 {
+    constexpr bool kExact = DT == kP32;
+    if (a.m >= 128 && a.n >= 128 && a.k >= 128 && a.a.ld < kTileMaxLd && a.b.ld < kTileMaxLd) {
+        const int64_t tiles = ((a.m + 255) / 256) * ((a.n + 255) / 256);
+        if (tiles < (int64_t)1 << 22) {
+            hipLaunchKernelGGL((product_tile_kernel<DT, kExact, 2, 4, 4, 2>), dim3((unsigned)tiles), dim3(512), 0, st, a);
+            return hipGetLastError();
+        }
+    }
     const int64_t tiles = ((a.n + 15) / 16) * ((a.m + 15) / 16);
     const unsigned grid = (unsigned)(tiles < (1 << 20) ? tiles : 1 << 20);
     hipLaunchKernelGGL((product_rows_kernel<DT, 1>), dim3(grid), dim3(256), 0, st, a);
