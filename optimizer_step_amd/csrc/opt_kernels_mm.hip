@@ -130,60 +130,79 @@ constexpr int64_t kTileMaxLd = (int64_t)1 << 23;   // keeps a tile's row offsets
 //
 // Tile i of a wave's T tiles takes its rows T r + i (r = lane % 32), so that
 // the scales of a lane's rows in all its tiles are neighbouring bytes: one
-// load brings them.  16-byte piece c of row R sits at c ^ ((R / T) % 8): the
-// reads of eight neighbouring lanes then fall into different banks.
+// load brings them.  In LDS a tile's 32 rows follow each other, 128 bytes
+// each, and 16-byte piece c of row r sits at c ^ (r / 2 % 8): sixteen
+// neighbouring lanes that read one piece of their rows then cover the 64 banks
+// once.
+template <int T>
+__host__ __device__ constexpr int lds_row_source(int p)     // the row that LDS row p holds
+{
+    return p / (32 * T) * (32 * T) + T * (p % 32) + p / 32 % T;
+}
+
 template <int ROWS, int T, int THREADS>
 struct StageCopy {
     static constexpr int kCopies = ROWS * 8 / THREADS;     // 16-byte pieces a thread copies
-    int off[kCopies];
+    static constexpr int kStep = THREADS / 8;              // LDS rows between them
+    static_assert(kStep % 32 == 0 && T % (kStep / 32) == 0, "a copy's rows are a constant distance on from the first's");
+    const uint8_t *p;      // the tile's first row
+    int ld, rows;          // rows of the tile that exist
+    int first;             // the thread's first piece
 
-    __device__ __forceinline__ void init(int64_t row0, int64_t rows, int64_t ld)
+    __device__ __forceinline__ void init(const Codes &q, int64_t row0, int64_t nrows)
     {
-#pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-            const int slot = i * THREADS + threadIdx.x, r = slot >> 3;
-            const int row = (int)min((int64_t)r, rows - 1 - row0);      // rows past the last repeat it; they are not stored
-            off[i] = row * (int)ld + 16 * ((slot & 7) ^ ((r / T) & 7));
-        }
+        p = q.codes + row0 * q.ld;
+        ld = (int)q.ld;
+        rows = (int)min((int64_t)ROWS, nrows - row0);
+        first = lds_row_source<T>(threadIdx.x >> 3) * ld + column();
     }
-    // p: the tile's first row
-    __device__ __forceinline__ void copy(const uint8_t *p, int k0, uint8_t *lds) const
+    // Column (byte) of a row at which this thread's pieces start.
+    __device__ __forceinline__ int column() const { return 16 * ((threadIdx.x & 7) ^ ((threadIdx.x >> 4) & 7)); }
+
+    // Rows past the last are outside the buffer that the loads are given: what
+    // their part of LDS then holds goes into rows of C that are not stored.
+    __device__ __forceinline__ void copy(int k0, uint8_t *lds) const
     {
-        const auto src = __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, 0x7FFFFFFF, 0x00027000);
+        const auto src = __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, rows * ld, 0x00027000);
 #pragma unroll
         for (int i = 0; i < kCopies; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (OPT_LDS void *)(lds + 16 * (i * THREADS + (threadIdx.x & ~63))), 16,
-                                                     off[i], k0, 0, 0);
+                                                     first, k0 + lds_row_source<T>(i * kStep) * ld, 0, 0);
     }
     // the last stage of rows that end inside it: pieces past the end are zeros
-    __device__ __forceinline__ void copy_tail(const uint8_t *p, uint8_t *lds, int left) const
+    __device__ __forceinline__ void copy_tail(int k0, uint8_t *lds, int left) const
     {
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) {
-            const int slot = i * THREADS + threadIdx.x, c = 16 * ((slot & 7) ^ ((slot >> 3) / T & 7));
             u4 v = {0, 0, 0, 0};
-            if (c < left) v = gld<u4>(p + off[i]);
-            *(u4 *)(lds + 16 * slot) = v;
+            const int row = lds_row_source<T>((int)(threadIdx.x >> 3) + i * kStep);
+            if (row < rows && column() < left) v = gld<u4>(p + k0 + row * ld + column());
+            *(u4 *)(lds + 16 * (i * THREADS + threadIdx.x)) = v;
         }
     }
 };
 
-// The T scale bytes of rows T r .. T r + T - 1 of a wave's rows.
+// The T scale bytes of rows T r .. T r + T - 1 of a wave's rows, first at
+// `row`; rows past the last read some of its.
 template <int T>
-__device__ __forceinline__ uint32_t row_scales(const Codes &q, int64_t block, int64_t row, int64_t rows)
+__device__ __forceinline__ uint32_t scale_row(int64_t row, int64_t rows)
 {
-    const int64_t at = min(row, ((rows + 3) & ~(int64_t)3) - 4 + (T == 4 ? 0 : 2));
-    const uint8_t *p = q.scales + block * q.lds + at;
-    return T == 4 ? gld<uint32_t>(p) : (uint32_t)gld<uint16_t>(p);
+    return (uint32_t)min(row, ((rows + 3) & ~(int64_t)3) - T);
+}
+
+template <int T>
+__device__ __forceinline__ uint32_t row_scales(const Codes &q, int block, uint32_t row)
+{
+    const uint8_t *p = q.scales + block * q.lds;
+    return T == 4 ? gld<uint32_t>(p + row) : (uint32_t)gld<uint16_t>(p + row);
 }
 
 // Where a lane's 32 bytes of either half (64 columns) of its row of tile 0 sit
-// in a stage; tile i's are i rows on, a constant the read instruction holds.
+// in a stage; tile i's are 32 i rows on, a constant the read instruction holds.
 struct LaneRow {
     int piece[2][2];
 
-    // first: the wave's first row, a multiple of 8 T
-    template <int T>
+    // first: the wave's first row
     __device__ __forceinline__ void init(int first)
     {
         const int r = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
@@ -191,15 +210,15 @@ struct LaneRow {
         for (int half = 0; half < 2; ++half)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                int o = (first + T * r) * kStage + 16 * ((4 * half + 2 * h + b) ^ (r & 7));
+                int o = (first + r) * kStage + 16 * ((4 * half + 2 * h + b) ^ ((r >> 1) & 7));
                 asm("" : "+v"(o));          // one register: not formed again from its parts for every tile
                 piece[half][b] = o;
             }
     }
     __device__ __forceinline__ i8v read(const uint8_t *lds, int i, int half) const
     {
-        const u4 lo = *(const u4 *)(lds + piece[half][0] + i * kStage);
-        const u4 hi = *(const u4 *)(lds + piece[half][1] + i * kStage);
+        const u4 lo = *(const u4 *)(lds + piece[half][0] + i * 32 * kStage);
+        const u4 hi = *(const u4 *)(lds + piece[half][1] + i * 32 * kStage);
         return (i8v){(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
     }
 };
@@ -209,26 +228,75 @@ __device__ __forceinline__ f16v mfma_codes(const i8v &b, int sb, const i8v &a, i
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 0, 0, 0, sb, 0, sa);
 }
 
-// One tile row of a half: acc[j] += fb[j] x fa.
-template <bool EXACT, int TN>
-__device__ __forceinline__ void multiply(f16v (&acc)[TN], const i8v &fa, const i8v (&fb)[TN], uint32_t sa, uint32_t sb)
-{
-    if (!EXACT) {
+// The B codes of one half as the matrix instructions take them: as they are,
+// or widened once for all tile rows.
+template <bool EXACT, int TN> struct HalfB;
+template <int TN> struct HalfB<false, TN> {
+    i8v v[TN];
+    __device__ __forceinline__ HalfB(const i8v (&fb)[TN], uint32_t)
+    {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) v[j] = fb[j];
+    }
+};
+template <int TN> struct HalfB<true, TN> {
+    bf8v v[TN][4];
+    __device__ __forceinline__ HalfB(const i8v (&fb)[TN], uint32_t sb)
+    {
 #pragma unroll
         for (int j = 0; j < TN; ++j)
-            acc[j] = mfma_codes(fb[j], (int)(sb >> (8 * j)), fa, (int)sa, acc[j]);
-    } else {
-        const float ma = scale_of(sa & 255u);
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                v[j][s] = widen8((uint32_t)fb[j][2 * s], (uint32_t)fb[j][2 * s + 1], scale_of((sb >> (8 * j)) & 255u));
+    }
+};
+
+#define SCHED() __builtin_amdgcn_sched_barrier(0)
+
+// A half's tile rows i = 0 .. TM - 1: acc[i][j] += b[j] x A's tile i.  fa holds
+// the codes of the next PF tile rows; `before(i)` runs ahead of tile row i, and
+// `next(i)` reads the codes that take the place of tile i's once those are
+// used.  The order of reads, conversions and
+// matrix instructions is pinned: left alone, the compiler moves every read
+// next to its use and the matrix cores wait for it.
+template <int TM, int TN, int PF, class Before, class Next>
+__device__ __forceinline__ void half_step(f16v (&acc)[TM][TN], i8v (&fa)[PF], const HalfB<false, TN> &b, uint32_t sa, uint32_t sb,
+                                          Before before, Next next)
+{
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        SCHED();
+        before(i);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = mfma_codes(b.v[j], (int)(sb >> (8 * j)), fa[i % PF], (int)(sa >> (8 * i)), acc[i][j]);
+        fa[i % PF] = next(i);
+    }
+    SCHED();
+}
+
+// The same with A widened 16 columns ahead of the instructions that take them.
+template <int TM, int TN, int PF, class Before, class Next>
+__device__ __forceinline__ void half_step(f16v (&acc)[TM][TN], i8v (&fa)[PF], const HalfB<true, TN> &b, uint32_t sa, uint32_t,
+                                          Before before, Next next)
+{
+    bf8v w = widen8((uint32_t)fa[0][0], (uint32_t)fa[0][1], scale_of(sa & 255u));
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        before(i);
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            const bf8v wa = widen8((uint32_t)fa[2 * s], (uint32_t)fa[2 * s + 1], ma);
+            SCHED();
+            bf8v n = w;
+            const int i1 = s < 3 ? i : i + 1, s1 = s < 3 ? s + 1 : 0;
+            if (i1 < TM)
+                n = widen8((uint32_t)fa[i1 % PF][2 * s1], (uint32_t)fa[i1 % PF][2 * s1 + 1], scale_of((sa >> (8 * i1)) & 255u));
+            if (s == 2) fa[i % PF] = next(i);
 #pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                const bf8v wb = widen8((uint32_t)fb[j][2 * s], (uint32_t)fb[j][2 * s + 1], scale_of((sb >> (8 * j)) & 255u));
-                acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb, wa, acc[j], 0, 0, 0);
-            }
+            for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b.v[j][s], w, acc[i][j], 0, 0, 0);
+            w = n;
         }
     }
+    SCHED();
 }
 
 // Every wave's copies into LDS and reads from it have ended.
@@ -238,9 +306,7 @@ __device__ __forceinline__ void stage_barrier()
     __syncthreads();
 }
 
-#define SCHED() __builtin_amdgcn_sched_barrier(0)
-
-template <int DT, bool EXACT, int WM, int WN, int TM, int TN>
+template <int DT, bool EXACT, int WM, int WN, int TM, int TN, int PF>
 __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(MatmulArgs a)
 {
 #if defined(__HIP_DEVICE_COMPILE__)   // the host pass has no buffer and matrix builtins, and needs the name alone
@@ -254,10 +320,10 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(MatmulArgs a
     (void)tm;
     StageCopy<BM, TM, kThr> ca;
     StageCopy<BN, TN, kThr> cb;
-    const uint8_t *pa = a.a.codes + m0 * a.a.ld, *pb = a.b.codes + n0 * a.b.ld;
-    ca.init(m0, a.m, a.a.ld);
-    cb.init(n0, a.n, a.b.ld);
+    ca.init(a.a, m0, a.m);
+    cb.init(a.b, n0, a.n);
     const int64_t ra = m0 + wm + TM * r, rb = n0 + wn + TN * r;
+    const uint32_t xa = scale_row<TM>(ra, a.m), xb = scale_row<TN>(rb, a.n);
     const int stages = (int)(a.k / kStage), last = stages - 1;
     f16v acc[TM][TN];
 #pragma unroll
@@ -268,44 +334,45 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(MatmulArgs a
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
     LaneRow la_row, lb_row;
-    la_row.init<TM>(wm);
-    lb_row.init<TN>(wn);
-    i8v fa[TM], fb0[TN], fb1[TN];
+    la_row.init(wm);
+    lb_row.init(wn);
+    i8v fa[PF], fb0[TN], fb1[TN];        // codes of A's next PF tile rows and of B's halves
     uint32_t sa, sb;
-    // One half: tile row i is multiplied, then the registers of its codes take
-    // the next half's.
-    auto half_step = [&](const i8v (&fb)[TN], i8v (&nb)[TN], const uint8_t *la, const uint8_t *lb, int half) {
-#pragma unroll
-        for (int j = 0; j < TN; ++j) nb[j] = lb_row.read(lb, j, half);
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            SCHED();
-            multiply<EXACT, TN>(acc[i], fa[i], fb, sa >> (8 * i), sb);
-            fa[i] = la_row.read(la, i, half);
-        }
-        SCHED();
-    };
-    // stage s is in (la, lb), its half 0 in registers; past the last stage it
-    // copies and reads that one again, which nothing uses
+    // stage s is in (la, lb), its half 0 of B and first tile rows of A in
+    // registers; past the last stage it copies and reads that one again, which
+    // nothing uses
     auto stage = [&](int s, uint8_t *la, uint8_t *lb, uint8_t *na, uint8_t *nb) {
-        const uint32_t ta = row_scales<TM>(a.a, min(s + 1, last), ra, a.m), tb = row_scales<TN>(a.b, min(s + 1, last), rb, a.n);
-        half_step(fb0, fb1, la, lb, 1);
-        stage_barrier();               // everyone's reads of this stage and copies of the next have ended
-        ca.copy(pa, min(s + 2, last) * kStage, la);
-        cb.copy(pb, min(s + 2, last) * kStage, lb);
-        half_step(fb1, fb0, na, nb, 0);
+        const uint32_t ta = row_scales<TM>(a.a, min(s + 1, last), xa), tb = row_scales<TN>(a.b, min(s + 1, last), xb);
+        {
+            const HalfB<EXACT, TN> b(fb0, sb);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) fb1[j] = lb_row.read(lb, j, 1);
+            auto next = [&](int i) { return i + PF < TM ? la_row.read(la, i + PF, 0) : la_row.read(la, i + PF - TM, 1); };
+            half_step<TM, TN, PF>(acc, fa, b, sa, sb, [](int) {}, next);
+        }
+        const HalfB<EXACT, TN> b(fb1, sb);
+        auto turn = [&](int i) {
+            if (i != TM - PF) return;
+            stage_barrier();           // everyone's reads of this stage and copies of the next have ended
+            ca.copy(min(s + 2, last) * kStage, la);
+            cb.copy(min(s + 2, last) * kStage, lb);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) fb0[j] = lb_row.read(nb, j, 0);
+        };
+        auto next = [&](int i) { return i + PF < TM ? la_row.read(la, i + PF, 1) : la_row.read(na, i + PF - TM, 0); };
+        half_step<TM, TN, PF>(acc, fa, b, sa, sb, turn, next);
         sa = ta;
         sb = tb;
     };
-    ca.copy(pa, 0, la0);
-    cb.copy(pb, 0, lb0);
+    ca.copy(0, la0);
+    cb.copy(0, lb0);
     stage_barrier();
-    ca.copy(pa, min(1, last) * kStage, la1);
-    cb.copy(pb, min(1, last) * kStage, lb1);
-    sa = row_scales<TM>(a.a, 0, ra, a.m);
-    sb = row_scales<TN>(a.b, 0, rb, a.n);
+    ca.copy(min(1, last) * kStage, la1);
+    cb.copy(min(1, last) * kStage, lb1);
+    sa = row_scales<TM>(a.a, 0, xa);
+    sb = row_scales<TN>(a.b, 0, xb);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) fa[i] = la_row.read(la0, i, 0);
+    for (int i = 0; i < PF; ++i) fa[i] = la_row.read(la0, i, 0);
 #pragma unroll
     for (int j = 0; j < TN; ++j) fb0[j] = lb_row.read(lb0, j, 0);
     int s = 0;
@@ -317,17 +384,19 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(MatmulArgs a
     if (a.k % kStage) {
         const int64_t k0 = (int64_t)stages * kStage;
         stage_barrier();
-        ca.copy_tail(pa + k0, la0, (int)(a.k - k0));
-        cb.copy_tail(pb + k0, lb0, (int)(a.k - k0));
-        sa = row_scales<TM>(a.a, stages, ra, a.m);
-        sb = row_scales<TN>(a.b, stages, rb, a.n);
+        ca.copy_tail((int)k0, la0, (int)(a.k - k0));
+        cb.copy_tail((int)k0, lb0, (int)(a.k - k0));
+        sa = row_scales<TM>(a.a, stages, xa);
+        sb = row_scales<TN>(a.b, stages, xb);
         stage_barrier();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
 #pragma unroll
             for (int j = 0; j < TN; ++j) fb0[j] = lb_row.read(lb0, j, half);
 #pragma unroll
-            for (int i = 0; i < TM; ++i) multiply<EXACT, TN>(acc[i], la_row.read(la0, i, half), fb0, sa >> (8 * i), sb);
+            for (int i = 0; i < PF; ++i) fa[i] = la_row.read(la0, i, half);
+            half_step<TM, TN, PF>(acc, fa, HalfB<EXACT, TN>(fb0, sb), sa, sb, [](int) {},
+                                  [&](int i) { return la_row.read(la0, min(i + PF, TM - 1), half); });
         }
     }
     // lane (r, h) holds rows TM r + i of C and, of the columns TN x + j, those
@@ -360,6 +429,9 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(MatmulArgs a
 #endif
 }
 
+#ifndef MM_PF
+#define MM_PF 2
+#endif
 template <int DT>
 static hipError_t launch_matmul_t(const MatmulArgs &a, hipStream_t st)
 {
@@ -367,7 +439,7 @@ static hipError_t launch_matmul_t(const MatmulArgs &a, hipStream_t st)
     if (a.m >= 128 && a.n >= 128 && a.k >= 128 && a.a.ld < kTileMaxLd && a.b.ld < kTileMaxLd) {
         const int64_t tiles = ((a.m + 255) / 256) * ((a.n + 255) / 256);
         if (tiles < (int64_t)1 << 22) {
-            hipLaunchKernelGGL((product_tile_kernel<DT, kExact, 2, 4, 4, 2>), dim3((unsigned)tiles), dim3(512), 0, st, a);
+            hipLaunchKernelGGL((product_tile_kernel<DT, kExact, 2, 4, 4, 2, MM_PF>), dim3((unsigned)tiles), dim3(512), 0, st, a);
             return hipGetLastError();
         }
     }
