@@ -155,7 +155,8 @@ def _check(status):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: a Stream object costs 2.8 us to make, more than a launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -479,9 +480,9 @@ def block_buffers(rows, cols, device="cuda"):
 
 
 def _on_device(t, what, dev):
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if t.device.index != dev:
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{what} must be a CUDA tensor")
         raise ValueError(f"{what} is on {t.device}, not on the current device cuda:{dev}")
 
 
@@ -506,6 +507,8 @@ def _like(t, what, like, rows, cols, dev):
     type and sides."""
     if t is None:
         return None, 0
+    if t.get_device() == dev and t.dtype == like.dtype and t.shape == like.shape and t.is_contiguous():
+        return t.data_ptr(), cols
     _on_device(t, what, dev)
     if t.dtype != like.dtype:
         raise ValueError(f"{what} is {t.dtype}, not {like.dtype}")
@@ -520,16 +523,19 @@ def _coded(pair, what, rows, cols, dev):
     if pair is None:
         return OptCodes()
     q, s = pair
-    for t, part in ((q, "codes"), (s, "scales")):
-        _on_device(t, f"{what} {part}", dev)
-        if t.dim() != 2 or t.element_size() != 1 or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError(f"{what} {part} must be a 2-D tensor of bytes with contiguous rows")
-    if q.shape[0] != rows or q.shape[1] < _round_up(cols, 16):
-        raise ValueError(f"{what} codes must be [{rows}, >= {_round_up(cols, 16)}], got {list(q.shape)}")
-    if s.shape[0] < (cols + CODE_BLOCK - 1) // CODE_BLOCK or s.shape[1] < _round_up(rows, 4):
-        raise ValueError(f"{what} scales must be [>= {(cols + CODE_BLOCK - 1) // CODE_BLOCK}, >= {_round_up(rows, 4)}], got {list(s.shape)}")
-    return OptCodes(q.data_ptr(), q.stride(0) if rows > 1 else _round_up(cols, 16), s.data_ptr(),
-                    s.stride(0) if s.shape[0] > 1 else _round_up(rows, 4))
+    if q.dim() != 2 or s.dim() != 2 or q.element_size() != 1 or s.element_size() != 1:
+        raise ValueError(f"{what} codes and scales must be 2-D tensors of bytes")
+    _on_device(q, f"{what} codes", dev)
+    _on_device(s, f"{what} scales", dev)
+    (qr, qc), (sr, sc), (ql, qs), (sl, ss) = q.shape, s.shape, q.stride(), s.stride()
+    if (qc > 1 and qs != 1) or (sc > 1 and ss != 1):
+        raise ValueError(f"{what} codes and scales must have contiguous rows")
+    width, height = (cols + 15) // 16 * 16, (rows + 3) // 4 * 4
+    if qr != rows or qc < width:
+        raise ValueError(f"{what} codes must be [{rows}, >= {width}], got {list(q.shape)}")
+    if sr < (cols + CODE_BLOCK - 1) // CODE_BLOCK or sc < height:
+        raise ValueError(f"{what} scales must be [>= {(cols + CODE_BLOCK - 1) // CODE_BLOCK}, >= {height}], got {list(s.shape)}")
+    return OptCodes(q.data_ptr(), ql if rows > 1 else width, s.data_ptr(), sl if sr > 1 else height)
 
 
 def opt_dropout(x, out, p, seed=0, offset=0, residual=None, index_base=0, stream=None):
@@ -539,13 +545,13 @@ def opt_dropout(x, out, p, seed=0, offset=0, residual=None, index_base=0, stream
     and residual are contiguous, of one type and size; out may be x or
     residual.  index_base (a multiple of 8): the index of x's first element in
     the whole tensor."""
-    dev = _device()
+    dev, n, dtype = _device(), x.numel(), x.dtype
     for t, what in ((x, "x"), (out, "out"), (residual, "residual")):
         if t is not None:
             _on_device(t, what, dev)
-            if not t.is_contiguous() or t.dtype != x.dtype or t.numel() != x.numel():
+            if not t.is_contiguous() or t.dtype != dtype or t.numel() != n:
                 raise ValueError(f"{what} must be contiguous, of x's type and size")
-    return _check(lib().opt_dropout(x.data_ptr(), _ptr(residual), out.data_ptr(), x.numel(), _dtype_code(x), float(p),
+    return _check(lib().opt_dropout(x.data_ptr(), _ptr(residual), out.data_ptr(), n, _dtype_code(x), float(p),
                                     int(seed) & (2**64 - 1), int(offset) & (2**64 - 1), int(index_base), _stream(stream)))
 
 

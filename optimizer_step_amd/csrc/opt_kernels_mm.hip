@@ -148,6 +148,7 @@ struct StageCopy {
     const uint8_t *p;      // the tile's first row
     int ld, rows;          // rows of the tile that exist
     int first;             // the thread's first piece
+    int wave_at;           // its wave's first byte in LDS (uniform)
 
     __device__ __forceinline__ void init(const Codes &q, int64_t row0, int64_t nrows)
     {
@@ -155,18 +156,19 @@ struct StageCopy {
         ld = (int)q.ld;
         rows = (int)min((int64_t)ROWS, nrows - row0);
         first = lds_row_source<T>(threadIdx.x >> 3) * ld + column();
+        wave_at = __builtin_amdgcn_readfirstlane((int)(threadIdx.x & ~63)) * 16;
     }
     // Column (byte) of a row at which this thread's pieces start.
     __device__ __forceinline__ int column() const { return 16 * ((threadIdx.x & 7) ^ ((threadIdx.x >> 4) & 7)); }
 
     // Rows past the last are outside the buffer that the loads are given: what
     // their part of LDS then holds goes into rows of C that are not stored.
-    __device__ __forceinline__ void copy(int k0, uint8_t *lds) const
+    __device__ __forceinline__ void copy(int k0, uint8_t *lds, int from = 0, int to = kCopies) const
     {
         const auto src = __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, rows * ld, 0x00027000);
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (OPT_LDS void *)(lds + 16 * (i * THREADS + (threadIdx.x & ~63))), 16,
+        for (int i = from; i < to; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (OPT_LDS void *)(lds + 16 * (i * THREADS) + wave_at), 16,
                                                      first, k0 + lds_row_source<T>(i * kStep) * ld, 0, 0);
     }
     // the last stage of rows that end inside it: pieces past the end are zeros
@@ -228,75 +230,96 @@ __device__ __forceinline__ f16v mfma_codes(const i8v &b, int sb, const i8v &a, i
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 0, 0, 0, sb, 0, sa);
 }
 
-// The B codes of one half as the matrix instructions take them: as they are,
-// or widened once for all tile rows.
-template <bool EXACT, int TN> struct HalfB;
-template <int TN> struct HalfB<false, TN> {
-    i8v v[TN];
-    __device__ __forceinline__ HalfB(const i8v (&fb)[TN], uint32_t)
+#define SCHED() __builtin_amdgcn_sched_barrier(0)
+
+// The operands of one half as the matrix instructions take them, and the half's
+// work: for its tile rows i = 0 .. TM - 1, acc[i][j] += b[j] x A's tile i.  fa
+// holds the codes of the next PF tile rows; `before(i)` runs ahead of tile row
+// i, and `next(i)` reads the codes that take the place of tile i's once those
+// are used.  The order of reads, conversions and matrix instructions is
+// pinned: left alone, the compiler moves every read next to its use and the
+// matrix cores wait for it.  fbn, san, sbn: B's codes and the scales of the
+// half after this one.
+template <bool EXACT, int TM, int TN, int PF> struct Half;
+
+// 8-bit products: the codes as they are, the scales in the instruction.
+template <int TM, int TN, int PF>
+struct Half<false, TM, TN, PF> {
+    __device__ __forceinline__ void start(const i8v (&)[PF], const i8v (&)[TN], uint32_t, uint32_t) {}
+
+    template <class Before, class Next>
+    __device__ __forceinline__ void step(f16v (&acc)[TM][TN], i8v (&fa)[PF], const i8v (&fb)[TN], uint32_t sa, uint32_t sb,
+                                         const i8v (&)[TN], uint32_t, uint32_t, Before before, Next next)
     {
 #pragma unroll
-        for (int j = 0; j < TN; ++j) v[j] = fb[j];
+        for (int i = 0; i < TM; ++i) {
+            SCHED();
+            before(i);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = mfma_codes(fb[j], (int)(sb >> (8 * j)), fa[i % PF], (int)(sa >> (8 * i)), acc[i][j]);
+            fa[i % PF] = next(i);
+        }
+        SCHED();
     }
 };
-template <int TN> struct HalfB<true, TN> {
-    bf8v v[TN][4];
-    __device__ __forceinline__ HalfB(const i8v (&fb)[TN], uint32_t sb)
+
+// Exact products: codes widened with their scales, A's sixteen columns ahead of
+// the instructions that take them, B's once for all tile rows, each part as
+// soon as the last tile row is done with the half before's.
+template <int TM, int TN, int PF>
+struct Half<true, TM, TN, PF> {
+    bf8v b[TN][4], w;
+
+    __device__ __forceinline__ void widen_b(const i8v (&fb)[TN], uint32_t sb, int s)
     {
 #pragma unroll
         for (int j = 0; j < TN; ++j)
+            b[j][s] = widen8((uint32_t)fb[j][2 * s], (uint32_t)fb[j][2 * s + 1], scale_of((sb >> (8 * j)) & 255u));
+    }
+    __device__ __forceinline__ void start(const i8v (&fa)[PF], const i8v (&fb)[TN], uint32_t sa, uint32_t sb)
+    {
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-                v[j][s] = widen8((uint32_t)fb[j][2 * s], (uint32_t)fb[j][2 * s + 1], scale_of((sb >> (8 * j)) & 255u));
+        for (int s = 0; s < 4; ++s) widen_b(fb, sb, s);
+        w = widen8((uint32_t)fa[0][0], (uint32_t)fa[0][1], scale_of(sa & 255u));
+    }
+
+    template <class Before, class Next>
+    __device__ __forceinline__ void step(f16v (&acc)[TM][TN], i8v (&fa)[PF], const i8v (&)[TN], uint32_t sa, uint32_t,
+                                         const i8v (&fbn)[TN], uint32_t san, uint32_t sbn, Before before, Next next)
+    {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            before(i);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                SCHED();
+                const int i1 = s < 3 ? i : i + 1, s1 = s < 3 ? s + 1 : 0;
+                const uint32_t byte = (i1 < TM ? sa >> (8 * i1) : san) & 255u;
+                const bf8v n = widen8((uint32_t)fa[i1 % PF][2 * s1], (uint32_t)fa[i1 % PF][2 * s1 + 1], scale_of(byte));
+                if (s == 2) fa[i % PF] = next(i);
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j][s], w, acc[i][j], 0, 0, 0);
+                w = n;
+                if (i == TM - 1 && s > 0) widen_b(fbn, sbn, s - 1);
+            }
+        }
+        widen_b(fbn, sbn, 3);
+        SCHED();
     }
 };
 
-#define SCHED() __builtin_amdgcn_sched_barrier(0)
+// Workgroups go to the eight XCDs in turn, each with an L2 of its own: every XCD
+// takes a run of neighbouring tiles, and runs walk bands of eight tile rows
+// column by column, so that the 32 tiles an XCD has in work share few rows of
+// A and B.
+struct Place { int m, n; };
 
-// A half's tile rows i = 0 .. TM - 1: acc[i][j] += b[j] x A's tile i.  fa holds
-// the codes of the next PF tile rows; `before(i)` runs ahead of tile row i, and
-// `next(i)` reads the codes that take the place of tile i's once those are
-// used.  The order of reads, conversions and
-// matrix instructions is pinned: left alone, the compiler moves every read
-// next to its use and the matrix cores wait for it.
-template <int TM, int TN, int PF, class Before, class Next>
-__device__ __forceinline__ void half_step(f16v (&acc)[TM][TN], i8v (&fa)[PF], const HalfB<false, TN> &b, uint32_t sa, uint32_t sb,
-                                          Before before, Next next)
+__device__ __forceinline__ Place tile_place(int t, int tm, int tn)
 {
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        SCHED();
-        before(i);
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = mfma_codes(b.v[j], (int)(sb >> (8 * j)), fa[i % PF], (int)(sa >> (8 * i)), acc[i][j]);
-        fa[i % PF] = next(i);
-    }
-    SCHED();
-}
-
-// The same with A widened 16 columns ahead of the instructions that take them.
-template <int TM, int TN, int PF, class Before, class Next>
-__device__ __forceinline__ void half_step(f16v (&acc)[TM][TN], i8v (&fa)[PF], const HalfB<true, TN> &b, uint32_t sa, uint32_t,
-                                          Before before, Next next)
-{
-    bf8v w = widen8((uint32_t)fa[0][0], (uint32_t)fa[0][1], scale_of(sa & 255u));
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        before(i);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            SCHED();
-            bf8v n = w;
-            const int i1 = s < 3 ? i : i + 1, s1 = s < 3 ? s + 1 : 0;
-            if (i1 < TM)
-                n = widen8((uint32_t)fa[i1 % PF][2 * s1], (uint32_t)fa[i1 % PF][2 * s1 + 1], scale_of((sa >> (8 * i1)) & 255u));
-            if (s == 2) fa[i % PF] = next(i);
-#pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b.v[j][s], w, acc[i][j], 0, 0, 0);
-            w = n;
-        }
-    }
-    SCHED();
+    const int tiles = tm * tn, x = t & 7, share = tiles >> 3, more = tiles & 7;
+    const int u = x * share + min(x, more) + (t >> 3);
+    const int band = u / (8 * tn), in = u - band * 8 * tn, height = min(8, tm - 8 * band);
+    return Place{8 * band + in % height, in / height};
 }
 
 // Every wave's copies into LDS and reads from it have ended.
@@ -312,12 +335,10 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(MatmulArgs a
 #if defined(__HIP_DEVICE_COMPILE__)   // the host pass has no buffer and matrix builtins, and needs the name alone
     constexpr int kThr = 64 * WM * WN, BM = 32 * TM * WM, BN = 32 * TN * WN;
     __shared__ __attribute__((aligned(16))) uint8_t la0[BM * kStage], la1[BM * kStage], lb0[BN * kStage], lb1[BN * kStage];
-    const int wave = threadIdx.x >> 6, r = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), r = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
     const int wm = (wave / WN) * 32 * TM, wn = (wave % WN) * 32 * TN;
-    const int64_t tm = (a.m + BM - 1) / BM, tn = (a.n + BN - 1) / BN;
-    const int64_t t = blockIdx.x;
-    const int64_t m0 = (t / tn) * BM, n0 = (t % tn) * BN;
-    (void)tm;
+    const Place at = tile_place(blockIdx.x, (int)((a.m + BM - 1) / BM), (int)((a.n + BN - 1) / BN));
+    const int64_t m0 = (int64_t)at.m * BM, n0 = (int64_t)at.n * BN;
     StageCopy<BM, TM, kThr> ca;
     StageCopy<BN, TN, kThr> cb;
     ca.init(a.a, m0, a.m);
@@ -337,44 +358,55 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(MatmulArgs a
     la_row.init(wm);
     lb_row.init(wn);
     i8v fa[PF], fb0[TN], fb1[TN];        // codes of A's next PF tile rows and of B's halves
+    Half<EXACT, TM, TN, PF> half;
     uint32_t sa, sb;
+    // The copies of a stage, spread over the PF + TM tile rows from the barrier
+    // to the end of the next half: all at once they would hold the waves up
+    // behind each other.
+    constexpr int kA = StageCopy<BM, TM, kThr>::kCopies, kB = StageCopy<BN, TN, kThr>::kCopies, kParts = PF + TM;
+    auto copy_part = [&](int part, int k0, uint8_t *la, uint8_t *lb) {
+#pragma unroll
+        for (int c = 0; c < kA + kB; ++c) {
+            if (c * kParts / (kA + kB) != part) continue;
+            if (c < kA) ca.copy(k0, la, c, c + 1);
+            else cb.copy(k0, lb, c - kA, c - kA + 1);
+        }
+    };
     // stage s is in (la, lb), its half 0 of B and first tile rows of A in
     // registers; past the last stage it copies and reads that one again, which
     // nothing uses
     auto stage = [&](int s, uint8_t *la, uint8_t *lb, uint8_t *na, uint8_t *nb) {
         const uint32_t ta = row_scales<TM>(a.a, min(s + 1, last), xa), tb = row_scales<TN>(a.b, min(s + 1, last), xb);
-        {
-            const HalfB<EXACT, TN> b(fb0, sb);
 #pragma unroll
-            for (int j = 0; j < TN; ++j) fb1[j] = lb_row.read(lb, j, 1);
-            auto next = [&](int i) { return i + PF < TM ? la_row.read(la, i + PF, 0) : la_row.read(la, i + PF - TM, 1); };
-            half_step<TM, TN, PF>(acc, fa, b, sa, sb, [](int) {}, next);
-        }
-        const HalfB<EXACT, TN> b(fb1, sb);
+        for (int j = 0; j < TN; ++j) fb1[j] = lb_row.read(lb, j, 1);
+        half.step(acc, fa, fb0, sa, sb, fb1, sa, sb,
+                  [&](int i) { copy_part(i + PF, min(s + 1, last) * kStage, na, nb); },
+                  [&](int i) { return i + PF < TM ? la_row.read(la, i + PF, 0) : la_row.read(la, i + PF - TM, 1); });
         auto turn = [&](int i) {
-            if (i != TM - PF) return;
-            stage_barrier();           // everyone's reads of this stage and copies of the next have ended
-            ca.copy(min(s + 2, last) * kStage, la);
-            cb.copy(min(s + 2, last) * kStage, lb);
+            if (i == TM - PF) {
+                stage_barrier();       // everyone's reads of this stage and copies of the next have ended
 #pragma unroll
-            for (int j = 0; j < TN; ++j) fb0[j] = lb_row.read(nb, j, 0);
+                for (int j = 0; j < TN; ++j) fb0[j] = lb_row.read(nb, j, 0);
+            }
+            if (i >= TM - PF) copy_part(i - (TM - PF), min(s + 2, last) * kStage, la, lb);
         };
-        auto next = [&](int i) { return i + PF < TM ? la_row.read(la, i + PF, 1) : la_row.read(na, i + PF - TM, 0); };
-        half_step<TM, TN, PF>(acc, fa, b, sa, sb, turn, next);
+        half.step(acc, fa, fb1, sa, sb, fb0, ta, tb, turn,
+                  [&](int i) { return i + PF < TM ? la_row.read(la, i + PF, 1) : la_row.read(na, i + PF - TM, 0); });
         sa = ta;
         sb = tb;
     };
     ca.copy(0, la0);
     cb.copy(0, lb0);
     stage_barrier();
-    ca.copy(min(1, last) * kStage, la1);
-    cb.copy(min(1, last) * kStage, lb1);
+#pragma unroll
+    for (int i = 0; i < PF; ++i) copy_part(i, min(1, last) * kStage, la1, lb1);
     sa = row_scales<TM>(a.a, 0, xa);
     sb = row_scales<TN>(a.b, 0, xb);
 #pragma unroll
     for (int i = 0; i < PF; ++i) fa[i] = la_row.read(la0, i, 0);
 #pragma unroll
     for (int j = 0; j < TN; ++j) fb0[j] = lb_row.read(lb0, j, 0);
+    half.start(fa, fb0, sa, sb);
     int s = 0;
     for (; s + 1 < stages; s += 2) {
         stage(s, la0, lb0, la1, lb1);
@@ -390,13 +422,13 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(MatmulArgs a
         sb = row_scales<TN>(a.b, stages, xb);
         stage_barrier();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int z = 0; z < 2; ++z) {
 #pragma unroll
-            for (int j = 0; j < TN; ++j) fb0[j] = lb_row.read(lb0, j, half);
+            for (int j = 0; j < TN; ++j) fb0[j] = lb_row.read(lb0, j, z);
 #pragma unroll
-            for (int i = 0; i < PF; ++i) fa[i] = la_row.read(la0, i, half);
-            half_step<TM, TN, PF>(acc, fa, HalfB<EXACT, TN>(fb0, sb), sa, sb, [](int) {},
-                                  [&](int i) { return la_row.read(la0, min(i + PF, TM - 1), half); });
+            for (int i = 0; i < PF; ++i) fa[i] = la_row.read(la0, i, z);
+            half.start(fa, fb0, sa, sb);
+            half.step(acc, fa, fb0, sa, sb, fb0, sa, sb, [](int) {}, [&](int i) { return la_row.read(la0, min(i + PF, TM - 1), z); });
         }
     }
     // lane (r, h) holds rows TM r + i of C and, of the columns TN x + j, those
@@ -429,24 +461,41 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(MatmulArgs a
 #endif
 }
 
-#ifndef MM_PF
-#define MM_PF 2
+template <int DT, int MT>
+static hipError_t launch_rows(const MatmulArgs &a, hipStream_t st)
+{
+    const int64_t tiles = ((a.n + 15) / 16) * ((a.m + 16 * MT - 1) / (16 * MT));
+    const unsigned grid = (unsigned)(tiles < (1 << 20) ? tiles : 1 << 20);
+    hipLaunchKernelGGL((product_rows_kernel<DT, MT>), dim3(grid), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+template <int DT, int WM, int WN, int TM, int TN, int PF>
+static hipError_t launch_tile(const MatmulArgs &a, hipStream_t st)
+{
+    constexpr int64_t BM = 32 * TM * WM, BN = 32 * TN * WN;
+    const int64_t tiles = ((a.m + BM - 1) / BM) * ((a.n + BN - 1) / BN);
+    hipLaunchKernelGGL((product_tile_kernel<DT, DT == kP32, WM, WN, TM, TN, PF>), dim3((unsigned)tiles), dim3(64 * WM * WN), 0, st, a);
+    return hipGetLastError();
+}
+
+#ifndef MM_FORCE
+#define MM_FORCE 0
 #endif
+
 template <int DT>
 static hipError_t launch_matmul_t(const MatmulArgs &a, hipStream_t st)
 {
-    constexpr bool kExact = DT == kP32;
-    if (a.m >= 128 && a.n >= 128 && a.k >= 128 && a.a.ld < kTileMaxLd && a.b.ld < kTileMaxLd) {
-        const int64_t tiles = ((a.m + 255) / 256) * ((a.n + 255) / 256);
-        if (tiles < (int64_t)1 << 22) {
-            hipLaunchKernelGGL((product_tile_kernel<DT, kExact, 2, 4, 4, 2, MM_PF>), dim3((unsigned)tiles), dim3(512), 0, st, a);
-            return hipGetLastError();
-        }
-    }
-    const int64_t tiles = ((a.n + 15) / 16) * ((a.m + 15) / 16);
-    const unsigned grid = (unsigned)(tiles < (1 << 20) ? tiles : 1 << 20);
-    hipLaunchKernelGGL((product_rows_kernel<DT, 1>), dim3(grid), dim3(256), 0, st, a);
-    return hipGetLastError();
+    const bool tiled = a.a.ld < kTileMaxLd && a.b.ld < kTileMaxLd && ((a.m + 127) / 128) * ((a.n + 127) / 128) < (1 << 22);
+    if (MM_FORCE == 1) return launch_rows<DT, 1>(a, st);
+    if (MM_FORCE == 2) return launch_rows<DT, 2>(a, st);
+    if (MM_FORCE == 3) return launch_rows<DT, 4>(a, st);
+    if (MM_FORCE == 4) return launch_tile<DT, 2, 2, 2, 2, 1>(a, st);
+    if (MM_FORCE == 5) return launch_tile<DT, 2, 2, 2, 2, 2>(a, st);
+    if (MM_FORCE == 6) return launch_tile<DT, 2, 4, 2, 2, 1>(a, st);
+    if (MM_FORCE == 7) return launch_tile<DT, 2, 4, 4, 2, 2>(a, st);
+    if (a.m >= 128 && a.n >= 128 && a.k >= 128 && tiled) return launch_tile<DT, 2, 4, 4, 2, 2>(a, st);
+    return launch_rows<DT, 1>(a, st);
 }
 
 hipError_t launch_block_matmul(int dt, const MatmulArgs &a, hipStream_t st)
