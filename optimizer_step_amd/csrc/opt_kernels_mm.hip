@@ -31,21 +31,34 @@ __device__ __forceinline__ bf8v widen8(uint32_t lo, uint32_t hi, float scale)
     return (bf8v){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// 32 code bytes of one row for a lane, widened.  Which 32 of the block's 128
-// columns they are does not matter to the sum as long as A and B agree: a lane
-// takes two 16-byte pieces 64 columns apart, so each quarter-wave reads 64
-// consecutive bytes.  Pieces past the row's end read as zero codes.
-struct Piece { bf8v v[4]; };
+// 32 code bytes of one row and their scale, for a lane.  Which 32 of the
+// block's 128 columns they are does not matter to the sum as long as A and B
+// agree: a lane takes two 16-byte pieces 64 columns apart, so each
+// quarter-wave reads 64 consecutive bytes.  WHOLE: the block lies inside the
+// row; else pieces past the row's end read as zero codes.
+struct Piece {
+    u4 lo, hi;
+    uint32_t byte;
 
-__device__ __forceinline__ Piece code_piece(const uint8_t *row, const uint8_t *scale, int64_t k0, int64_t k, int part)
-{
-    const u4 z = {0, 0, 0, 0};
-    const int64_t p = k0 + 16 * part;
-    const u4 lo = p < k ? gld<u4>(row + p) : z;
-    const u4 hi = p + 64 < k ? gld<u4>(row + p + 64) : z;
-    const float s = scale_of(gld<uint8_t>(scale));
-    return Piece{{widen8(lo[0], lo[1], s), widen8(lo[2], lo[3], s), widen8(hi[0], hi[1], s), widen8(hi[2], hi[3], s)}};
-}
+    template <bool WHOLE>
+    __device__ __forceinline__ void load(const Codes &q, int64_t row, int64_t block, int64_t k, int part)
+    {
+        const uint8_t *p = q.codes + row * q.ld + block * 128 + 16 * part;
+        const int64_t left = k - block * 128 - 16 * part;
+        lo = hi = (u4){0, 0, 0, 0};
+        if (WHOLE || left > 0) lo = gld<u4>(p);
+        if (WHOLE || left > 64) hi = gld<u4>(p + 64);
+        byte = gld<uint8_t>(q.scales + block * q.lds + row);
+    }
+    __device__ __forceinline__ void widen(bf8v v[4]) const
+    {
+        const float s = scale_of(byte);
+        v[0] = widen8(lo[0], lo[1], s);
+        v[1] = widen8(lo[2], lo[3], s);
+        v[2] = widen8(hi[0], hi[1], s);
+        v[3] = widen8(hi[2], hi[3], s);
+    }
+};
 
 template <int DT>
 __device__ __forceinline__ void store_c(const MatmulArgs &a, int64_t m, int64_t n, f4 v)
@@ -68,13 +81,41 @@ __device__ __forceinline__ void store_c(const MatmulArgs &a, int64_t m, int64_t 
 }
 
 // A workgroup of four waves forms 16 x MT rows of A by 16 of B; each wave sums
-// every fourth block of 128 columns and the four sums meet in LDS.
+// every fourth block of 128 columns and the four sums meet in LDS.  It is bound
+// by the read of B: a wave has the pieces of kAhead blocks in flight.
+constexpr int kAhead = 4;
+
+template <int MT, int U, bool WHOLE>
+__device__ __forceinline__ void rows_blocks(const MatmulArgs &a, f4 (&acc)[MT], int64_t nr, const int64_t (&mr)[MT], int64_t block,
+                                            int part)
+{
+    Piece b[U], x[U][MT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        b[u].template load<WHOLE>(a.b, nr, block + 4 * u, a.k, part);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) x[u][i].template load<WHOLE>(a.a, mr[i], block + 4 * u, a.k, part);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        bf8v vb[4], va[4];
+        b[u].widen(vb);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            x[u][i].widen(va);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb[j], va[j], acc[i], 0, 0, 0);
+        }
+    }
+}
+
 template <int DT, int MT>
 __global__ __launch_bounds__(256) void product_rows_kernel(MatmulArgs a)
 {
     __shared__ f4 sum[3][MT][64];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, part = lane >> 4;
     const int64_t tn = (a.n + 15) / 16, tiles = tn * ((a.m + 16 * MT - 1) / (16 * MT));
+    const int64_t blocks = (a.k + 127) / 128, whole = a.k / 128;
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
         const int64_t n0 = (t % tn) * 16, m0 = (t / tn) * (16 * MT);
         const int64_t nr = min(n0 + r, a.n - 1);
@@ -85,15 +126,9 @@ __global__ __launch_bounds__(256) void product_rows_kernel(MatmulArgs a)
             mr[i] = min(m0 + 16 * i + r, a.m - 1);
             acc[i] = (f4){0, 0, 0, 0};
         }
-        for (int64_t k0 = 128 * wave; k0 < a.k; k0 += 512) {
-            const Piece b = code_piece(a.b.codes + nr * a.b.ld, a.b.scales + (k0 / 128) * a.b.lds + nr, k0, a.k, part);
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const Piece x = code_piece(a.a.codes + mr[i] * a.a.ld, a.a.scales + (k0 / 128) * a.a.lds + mr[i], k0, a.k, part);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[j], x.v[j], acc[i], 0, 0, 0);
-            }
-        }
+        int64_t block = wave;
+        for (; block + 4 * (kAhead - 1) < whole; block += 4 * kAhead) rows_blocks<MT, kAhead, true>(a, acc, nr, mr, block, part);
+        for (; block < blocks; block += 4) rows_blocks<MT, 1, false>(a, acc, nr, mr, block, part);
         __syncthreads();
         if (wave > 0)
 #pragma unroll
@@ -479,23 +514,28 @@ static hipError_t launch_tile(const MatmulArgs &a, hipStream_t st)
     return hipGetLastError();
 }
 
-#ifndef MM_FORCE
-#define MM_FORCE 0
-#endif
-
+// Which kernel: measured over 1 <= m <= 2048 by 500 .. 11008 columns of C by
+// k = 1024 .. 11008 (times at n = k = 4096, bf16 results, unless said).
+//
+// The rows kernel reads B once for every 32 rows of A at about 0.36 us per 10^6
+// bytes of it; a 128 x 128 tile takes about 0.6 us for each 128 columns of k
+// (1.1 us of exact products) whatever the rows, until the tiles fill the chip:
+// 64 rows 16.1 us against 16.3, 128 rows 26.4 against 16.4.  Equal at
+// ceil(m / 32) * n = 13000 (24000).
+//
+// 256 x 256 tiles read A and B half as often and run at twice the rate once
+// each compute unit has one; a round of them costs 45 us where 512 tiles of
+// 128 x 128, two a compute unit, cost 33 and up to 256 of them 28: 2048 rows
+// 46 us against 36, 11008 columns by 1024 rows 48 against 58.
 template <int DT>
 static hipError_t launch_matmul_t(const MatmulArgs &a, hipStream_t st)
 {
-    const bool tiled = a.a.ld < kTileMaxLd && a.b.ld < kTileMaxLd && ((a.m + 127) / 128) * ((a.n + 127) / 128) < (1 << 22);
-    if (MM_FORCE == 1) return launch_rows<DT, 1>(a, st);
-    if (MM_FORCE == 2) return launch_rows<DT, 2>(a, st);
-    if (MM_FORCE == 3) return launch_rows<DT, 4>(a, st);
-    if (MM_FORCE == 4) return launch_tile<DT, 2, 2, 2, 2, 1>(a, st);
-    if (MM_FORCE == 5) return launch_tile<DT, 2, 2, 2, 2, 2>(a, st);
-    if (MM_FORCE == 6) return launch_tile<DT, 2, 4, 2, 2, 1>(a, st);
-    if (MM_FORCE == 7) return launch_tile<DT, 2, 4, 4, 2, 2>(a, st);
-    if (a.m >= 128 && a.n >= 128 && a.k >= 128 && tiled) return launch_tile<DT, 2, 4, 4, 2, 2>(a, st);
-    return launch_rows<DT, 1>(a, st);
+    const int64_t small = ((a.m + 127) / 128) * ((a.n + 127) / 128), large = ((a.m + 255) / 256) * ((a.n + 255) / 256);
+    const bool fits = a.a.ld < kTileMaxLd && a.b.ld < kTileMaxLd && small < (1 << 22) && a.m >= 4 && a.n >= 4 && a.k >= kStage;
+    if (!fits || ((a.m + 31) / 32) * a.n <= (DT == kP32 ? 24000 : 13000))
+        return a.m <= 16 ? launch_rows<DT, 1>(a, st) : launch_rows<DT, 2>(a, st);
+    const int64_t tall = (large + 255) / 256 * 45, low = small <= 256 ? 28 : (small + 511) / 512 * 33;
+    return tall <= low ? launch_tile<DT, 2, 4, 4, 2, 2>(a, st) : launch_tile<DT, 2, 2, 2, 2, 1>(a, st);
 }
 
 hipError_t launch_block_matmul(int dt, const MatmulArgs &a, hipStream_t st)
