@@ -145,6 +145,7 @@ int opt_rms_norm(const opt_norm *n, void *stream)
     a.q = codes_of(n->q);
     a.w_dtype = n->w_dtype;
     a.eps = n->eps;
+    a.inv_cols = 1.0 / (double)n->cols;
     return done(launch_rms_norm(n->dtype, a, (hipStream_t)stream), "RMS norm launch");
 }
 
@@ -202,6 +203,7 @@ int opt_rms_norm_backward(const opt_norm_grad *n, void *stream)
     a.part = n->dweight ? (float *)n->workspace : nullptr;
     a.w_dtype = n->w_dtype;
     a.eps = n->eps;
+    a.inv_cols = 1.0 / (double)n->cols;
     return done(launch_rms_norm_grad(n->dtype, a, n->dweight, n->accumulate, (hipStream_t)stream), "RMS norm backward launch");
 }
 

@@ -16,62 +16,133 @@
 
 namespace optstep {
 
-// Sum over the LANES lanes of a row, the same bits in every lane; `slot` is
-// LDS scratch of a double per wave, used twice per call site at most.
-template <int LANES>
-__device__ __forceinline__ double row_sum(double v, double *slot)
+__device__ __forceinline__ double two_words(uint32_t lo, uint32_t hi) { return __hiloint2double((int)hi, (int)lo); }
+
+template <int CTRL>
+__device__ __forceinline__ double dpp_add(double x)
 {
-#pragma unroll
-    for (int off = 1; off < (LANES < 64 ? LANES : 64); off <<= 1) v += __shfl_xor(v, off, 64);
-    if (LANES > 64) {
-        __syncthreads();
-        if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = 0.0;
-        for (int w = 0; w < LANES / 64; ++w) v += slot[w];
+    const uint32_t lo = (uint32_t)__double2loint(x), hi = (uint32_t)__double2hiint(x);
+    return x + two_words((uint32_t)__builtin_amdgcn_mov_dpp((int)lo, CTRL, 0xF, 0xF, true),
+                         (uint32_t)__builtin_amdgcn_mov_dpp((int)hi, CTRL, 0xF, 0xF, true));
+}
+
+// Sum over 16 or 64 lanes, the same bits in every lane: each step adds two
+// partial sums that both sides hold (lanes 1, 2, 7 - i and 15 - i away by DPP;
+// then the rows and the halves of the wave by gfx950's lane swaps).
+template <int LANES>
+__device__ __forceinline__ double lanes_sum(double x)
+{
+    x = dpp_add<0xB1>(x);
+    x = dpp_add<0x4E>(x);
+    x = dpp_add<0x141>(x);
+    x = dpp_add<0x140>(x);
+    if (LANES >= 64) {
+        uint32_t lo = (uint32_t)__double2loint(x), hi = (uint32_t)__double2hiint(x);
+        auto l = __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+        auto h = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+        x = two_words(l[0], h[0]) + two_words(l[1], h[1]);
+        lo = (uint32_t)__double2loint(x);
+        hi = (uint32_t)__double2hiint(x);
+        l = __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
+        h = __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+        x = two_words(l[0], h[0]) + two_words(l[1], h[1]);
     }
-    return v;
+    return x;
+}
+
+// 1/sqrt(x) to within 2^-51: the hardware's estimate and two Newton steps, a
+// tenth of the instructions of a division after a square root (each of which
+// every wave would run once a row: 33 -> 29 us of a pass over 8192 x 4096).
+// Where a step has no value (x zero or infinite) the estimate is the result.
+__device__ __forceinline__ double inverse_root(double x)
+{
+    const double y0 = __builtin_amdgcn_rsq(x);
+    double y = y0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const double e = __builtin_fma(-x * y, y, 1.0);
+        y = __builtin_fma(0.5 * y, e, y);
+    }
+    return y == y ? y : y0;
 }
 
 constexpr int norm_threads(int lanes) { return lanes < 256 ? 256 : lanes; }
 
-template <int DT, int LANES, int VECS>
+// The sums of a row over its LANES lanes, in every lane.  Waves meet in `slot`
+// (N doubles a wave): one barrier, as consecutive calls take alternate slots.
+template <int LANES, int N>
+__device__ __forceinline__ void row_sums(double (&v)[N], double (*slot)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = lanes_sum<LANES>(v[i]);
+    if (LANES > 64) {
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) slot[threadIdx.x >> 6][i] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = slot[0][i];
+#pragma unroll
+        for (int w = 1; w < LANES / 64; ++w)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += slot[w][i];
+    }
+}
+
+template <int DT, int LANES, int VECS, bool EIGHTS>
 __global__ __launch_bounds__(norm_threads(LANES)) void rms_norm_kernel(NormArgs a)
 {
     constexpr int kRows = norm_threads(LANES) / LANES;   // rows a workgroup holds at once
-    __shared__ double slot[16];
+    __shared__ double slot[2][16][1];
     const int lane = threadIdx.x % LANES;
-    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.rows; r0 += (int64_t)gridDim.x * kRows) {
+    int turn = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.rows; r0 += (int64_t)gridDim.x * kRows, turn ^= 1) {
         const int64_t row = r0 + threadIdx.x / LANES;
         const bool live = row < a.rows;
-        float h[VECS][8];
-        double ss = 0.0;
+        constexpr bool kEarly = VECS <= 2;      // the weight waits in registers where there are some
+        float h[VECS][8], w[kEarly ? VECS : 1][8];
+        double ss[1] = {0.0};
 #pragma unroll
         for (int j = 0; j < VECS; ++j) {
             const int64_t c = 8 * (int64_t)(lane + j * LANES);
-            const int cnt = live ? left8(c, a.cols) : 0;
-            load8<DT>(a.x, row * a.ldx + c, cnt, h[j]);
-            if (a.res) {
-                float t[8];
-                load8<DT>(a.res, row * a.ldr + c, cnt, t);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) h[j][i] = stored<DT>(h[j][i] + t[i]);
-            }
-            if (a.h) store8<DT>(a.h, row * a.ldh + c, cnt, h[j]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = __builtin_fma((double)h[j][i], (double)h[j][i], ss);
+            load8<DT, EIGHTS>(a.x, row * a.ldx + c, live ? left8(c, a.cols) : 0, h[j]);
         }
-        ss = row_sum<LANES>(ss, slot);
-        const float r = (float)(1.0 / sqrt(ss / (double)a.cols + a.eps));
+        if (a.res) {
+            float t[VECS][8];
+#pragma unroll
+            for (int j = 0; j < VECS; ++j) {
+                const int64_t c = 8 * (int64_t)(lane + j * LANES);
+                load8<DT, EIGHTS>(a.res, row * a.ldr + c, live ? left8(c, a.cols) : 0, t[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < VECS; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[j][i] = stored<DT>(h[j][i] + t[j][i]);
+        }
+        if (kEarly)
+#pragma unroll
+            for (int j = 0; j < VECS; ++j) {
+                const int64_t c = 8 * (int64_t)(lane + j * LANES);
+                load8_any<EIGHTS>(a.w_dtype, a.w, c, left8(c, a.cols), w[j * kEarly]);
+            }
+#pragma unroll
+        for (int j = 0; j < VECS; ++j) {
+            const int64_t c = 8 * (int64_t)(lane + j * LANES);
+            if (a.h) store8<DT, EIGHTS>(a.h, row * a.ldh + c, live ? left8(c, a.cols) : 0, h[j]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss[0] = __builtin_fma((double)h[j][i], (double)h[j][i], ss[0]);
+        }
+        row_sums<LANES, 1>(ss, slot[turn]);
+        const float r = (float)inverse_root(__builtin_fma(ss[0], a.inv_cols, a.eps));
 #pragma unroll
         for (int j = 0; j < VECS; ++j) {
             const int64_t c = 8 * (int64_t)(lane + j * LANES);
             const int cnt = live ? left8(c, a.cols) : 0;
-            float w[8], y[8];
-            load8_any(a.w_dtype, a.w, c, left8(c, a.cols), w);
+            float y[8];
+            if (!kEarly) load8_any<EIGHTS>(a.w_dtype, a.w, c, left8(c, a.cols), w[0]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = i < cnt ? (h[j][i] * r) * w[i] : 0.0f;
-            if (a.y) store8<DT>(a.y, row * a.ldy + c, cnt, y);
+            for (int i = 0; i < 8; ++i) y[i] = i < cnt ? (h[j][i] * r) * w[j * kEarly][i] : 0.0f;
+            if (a.y) store8<DT, EIGHTS>(a.y, row * a.ldy + c, cnt, y);
             if (a.q.codes) {
                 const uint32_t byte = block_scale(row16_max_u32(abs_max8(y)));
                 const u2 code = encode8(y, byte);
@@ -82,52 +153,83 @@ __global__ __launch_bounds__(norm_threads(LANES)) void rms_norm_kernel(NormArgs 
     }
 }
 
-template <int DT, int LANES, int VECS>
+// A row of the backward pass as it is stored.
+template <int DT, int VECS>
+struct GradRow { Raw<DT> h[VECS], dy[VECS], dh[VECS]; };
+
+template <int DT, int LANES, int VECS, bool EIGHTS>
+__device__ __forceinline__ void load_row(const NormGradArgs &a, int64_t row, GradRow<DT, VECS> &g)
+{
+#pragma unroll
+    for (int j = 0; j < VECS; ++j) {
+        const int64_t c = 8 * (int64_t)(threadIdx.x % LANES + j * LANES);
+        const int cnt = row < a.rows ? left8(c, a.cols) : 0;
+        g.h[j] = load_raw<DT, EIGHTS>(a.h, row * a.ldh + c, cnt);
+        g.dy[j] = load_raw<DT, EIGHTS>(a.dy, row * a.lddy + c, cnt);
+        if (a.dh) g.dh[j] = load_raw<DT, EIGHTS>(a.dh, row * a.lddh + c, cnt);
+    }
+}
+
+// A workgroup takes every gridDim.x-th row (or group of rows) and keeps its
+// columns' sums of dy * (h * r) in registers; where two rows fit there, the
+// next one is on its way while this one's sums are formed.
+template <int DT, int LANES, int VECS, bool EIGHTS>
 __global__ __launch_bounds__(norm_threads(LANES)) void rms_norm_grad_kernel(NormGradArgs a)
 {
     constexpr int kRows = norm_threads(LANES) / LANES;
-    __shared__ double slot[16], slot2[16];
+    constexpr bool kAhead = VECS * (int)sizeof(typename Elem<DT>::T) <= 8;
+    __shared__ double slot[2][16][2];
     __shared__ float comb[LANES < 256 ? 256 * 8 : 1];
     const int lane = threadIdx.x % LANES;
+    const int64_t step = (int64_t)gridDim.x * kRows;
     float dw[VECS][8] = {};
-    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.rows; r0 += (int64_t)gridDim.x * kRows) {
-        const int64_t row = r0 + threadIdx.x / LANES;
+    int turn = 0;
+    int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / LANES;
+    GradRow<DT, VECS> g, next;
+    load_row<DT, LANES, VECS, EIGHTS>(a, row, g);
+    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.rows; r0 += step, row += step, turn ^= 1) {
         const bool live = row < a.rows;
-        float h[VECS][8], dy[VECS][8];
-        double ss = 0.0, gh = 0.0;
+        if (kAhead) load_row<DT, LANES, VECS, EIGHTS>(a, row + step, next);
+        else if (turn || r0 >= step) load_row<DT, LANES, VECS, EIGHTS>(a, row, g);
+        double s[2] = {0.0, 0.0};
+#pragma unroll
+        for (int j = 0; j < VECS; ++j) {
+            const int64_t c = 8 * (int64_t)(lane + j * LANES);
+            float w[8], h[8], dy[8];
+            load8_any<EIGHTS>(a.w_dtype, a.w, c, left8(c, a.cols), w);
+            unpack_raw<DT>(g.h[j], h);
+            unpack_raw<DT>(g.dy[j], dy);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                s[0] = __builtin_fma((double)h[i], (double)h[i], s[0]);
+                s[1] = __builtin_fma((double)(dy[i] * w[i]), (double)h[i], s[1]);
+            }
+        }
+        row_sums<LANES, 2>(s, slot[turn]);
+        const float r = (float)inverse_root(__builtin_fma(s[0], a.inv_cols, a.eps));
+        const float k = (float)((double)r * (double)r * (s[1] * a.inv_cols));
 #pragma unroll
         for (int j = 0; j < VECS; ++j) {
             const int64_t c = 8 * (int64_t)(lane + j * LANES);
             const int cnt = live ? left8(c, a.cols) : 0;
-            float w[8];
-            load8<DT>(a.h, row * a.ldh + c, cnt, h[j]);
-            load8<DT>(a.dy, row * a.lddy + c, cnt, dy[j]);
-            load8_any(a.w_dtype, a.w, c, left8(c, a.cols), w);
+            float w[8], h[8], dy[8], dx[8];
+            load8_any<EIGHTS>(a.w_dtype, a.w, c, left8(c, a.cols), w);
+            unpack_raw<DT>(g.h[j], h);
+            unpack_raw<DT>(g.dy[j], dy);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                ss = __builtin_fma((double)h[j][i], (double)h[j][i], ss);
-                gh = __builtin_fma((double)(dy[j][i] * w[i]), (double)h[j][i], gh);
+                dx[i] = r * (dy[i] * w[i] - h[i] * k);
+                if (live) dw[j][i] += dy[i] * (h[i] * r);
             }
-        }
-        ss = row_sum<LANES>(ss, slot);
-        gh = row_sum<LANES>(gh, slot2);
-        const float r = (float)(1.0 / sqrt(ss / (double)a.cols + a.eps));
-        const float k = (float)((double)r * (double)r * (gh / (double)a.cols));
+            if (a.dh) {
+                float t[8];
+                unpack_raw<DT>(g.dh[j], t);
 #pragma unroll
-        for (int j = 0; j < VECS; ++j) {
-            const int64_t c = 8 * (int64_t)(lane + j * LANES);
-            const int cnt = live ? left8(c, a.cols) : 0;
-            float w[8], t[8] = {}, dx[8];
-            load8_any(a.w_dtype, a.w, c, left8(c, a.cols), w);
-            if (a.dh) load8<DT>(a.dh, row * a.lddh + c, cnt, t);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                dx[i] = r * (dy[j][i] * w[i] - h[j][i] * k);
-                if (a.dh) dx[i] = dx[i] + t[i];
-                if (live) dw[j][i] += dy[j][i] * (h[j][i] * r);
+                for (int i = 0; i < 8; ++i) dx[i] = dx[i] + t[i];
             }
-            store8<DT>(a.dx, row * a.lddx + c, cnt, dx);
+            store8<DT, EIGHTS>(a.dx, row * a.lddx + c, cnt, dx);
         }
+        if (kAhead) g = next;
     }
     if (!a.part) return;
     // the workgroup's partial sums: rows of one wave by shuffles, then waves
@@ -159,25 +261,32 @@ __global__ __launch_bounds__(norm_threads(LANES)) void rms_norm_grad_kernel(Norm
     }
 }
 
-// dw[c] (+)= sum over the groups' partials, in binary64 and a fixed order: 64
-// columns a workgroup, four waves a quarter of the groups each.
-__global__ __launch_bounds__(256) void norm_dw_kernel(const float *part, int64_t groups, int64_t cols, float *dw, int accumulate)
+// dw[c] (+)= sum over the groups' partials, in binary64 and a fixed order: 32
+// columns a workgroup, 32 half-waves every 32nd group each.
+constexpr int kDwCols = 32;
+
+__global__ __launch_bounds__(1024) void norm_dw_kernel(const float *part, int64_t groups, int64_t cols, float *dw, int accumulate)
 {
-    __shared__ double s[4][64];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    __shared__ double s[32][kDwCols];
+    const int lane = threadIdx.x % kDwCols, rank = threadIdx.x / kDwCols;
+    const int64_t c = (int64_t)blockIdx.x * kDwCols + lane;
     double v = 0.0;
-    if (c < cols)
-        for (int64_t g = wave; g < groups; g += 4) v += (double)gld<float>(part + g * cols + c);
-    s[wave][lane] = v;
+    if (c < cols) {
+#pragma unroll 8
+        for (int64_t g = rank; g < groups; g += 32) v += (double)gld<float>(part + g * cols + c);
+    }
+    s[rank][lane] = v;
     __syncthreads();
-    if (wave == 0 && c < cols) {
-        v = ((s[0][lane] + s[1][lane]) + s[2][lane]) + s[3][lane];
+    if (rank == 0 && c < cols) {
+        for (int i = 1; i < 32; ++i) v += s[i][lane];
         if (accumulate) v += (double)gld<float>(dw + c);
         gst<float>(dw + c, (float)v);
     }
 }
 
+#ifndef NG
+#define NG 1024
+#endif
 NormShape norm_shape(int64_t cols)
 {
     const int64_t v = (cols + 7) / 8;                 // groups of eight in a row
@@ -193,7 +302,7 @@ int64_t norm_grad_groups(int64_t rows, int64_t cols)
     const NormShape s = norm_shape(cols);
     const int64_t per = s.lanes < 256 ? 256 / s.lanes : 1;
     const int64_t n = (rows + per - 1) / per;
-    const int64_t most = s.lanes == 1024 ? 256 : 1024;
+    const int64_t most = s.lanes == 1024 ? 256 : NG;
     return n < most ? n : most;
 }
 
@@ -208,7 +317,8 @@ static hipError_t launch_norm_t(const NormArgs &a, hipStream_t st)
     const unsigned grid = (unsigned)(want < (1 << 20) ? want : 1 << 20);
 #define X(L, V) \
     if (s.lanes == L && s.vecs == V) { \
-        hipLaunchKernelGGL((rms_norm_kernel<DT, L, V>), dim3(grid), dim3(norm_threads(L)), 0, st, a); \
+        if (a.cols % 8 == 0) hipLaunchKernelGGL((rms_norm_kernel<DT, L, V, true>), dim3(grid), dim3(norm_threads(L)), 0, st, a); \
+        else hipLaunchKernelGGL((rms_norm_kernel<DT, L, V, false>), dim3(grid), dim3(norm_threads(L)), 0, st, a); \
         return hipGetLastError(); \
     }
     NORM_SHAPES(X)
@@ -223,7 +333,8 @@ static hipError_t launch_norm_grad_t(const NormGradArgs &a, hipStream_t st)
     const unsigned grid = (unsigned)norm_grad_groups(a.rows, a.cols);
 #define X(L, V) \
     if (s.lanes == L && s.vecs == V) { \
-        hipLaunchKernelGGL((rms_norm_grad_kernel<DT, L, V>), dim3(grid), dim3(norm_threads(L)), 0, st, a); \
+        if (a.cols % 8 == 0) hipLaunchKernelGGL((rms_norm_grad_kernel<DT, L, V, true>), dim3(grid), dim3(norm_threads(L)), 0, st, a); \
+        else hipLaunchKernelGGL((rms_norm_grad_kernel<DT, L, V, false>), dim3(grid), dim3(norm_threads(L)), 0, st, a); \
         return hipGetLastError(); \
     }
     NORM_SHAPES(X)
@@ -245,7 +356,7 @@ hipError_t launch_rms_norm_grad(int dt, const NormGradArgs &a, float *dw, int ac
                                                                                     : launch_norm_grad_t<kPF16>(a, st);
     if (e != hipSuccess || !dw) return e;
     const int64_t groups = a.rows > 0 ? norm_grad_groups(a.rows, a.cols) : 0;
-    hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((a.cols + 63) / 64)), dim3(256), 0, st, (const float *)a.part, groups,
+    hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((a.cols + kDwCols - 1) / kDwCols)), dim3(1024), 0, st, (const float *)a.part, groups,
                        a.cols, dw, accumulate);
     return hipGetLastError();
 }

@@ -36,7 +36,7 @@ struct NormArgs {
     int64_t ldx, ldr, ldh, ldy;
     Codes q;
     int w_dtype;
-    double eps;
+    double eps, inv_cols;  // inv_cols: 1 / cols
 };
 
 struct NormGradArgs {
@@ -46,7 +46,7 @@ struct NormGradArgs {
     int64_t lddy, ldh, lddh, lddx;
     float *part;           // [groups][cols] partial sums of the weight's gradient, or null
     int w_dtype;
-    double eps;
+    double eps, inv_cols;  // inv_cols: 1 / cols
 };
 
 struct CastArgs {
@@ -82,6 +82,9 @@ template <> struct Elem<kPF16> { typedef uint16_t T; };
 typedef u4 u4_any __attribute__((aligned(2)));
 typedef u2 u2_any __attribute__((aligned(2)));
 
+// Eight elements as they are stored.
+template <int DT> struct Raw { u4 v[DT == kP32 ? 2 : 1]; };
+
 template <int DT>
 __device__ __forceinline__ void unpack8(const uint32_t w[4], float v[8])
 {
@@ -108,36 +111,62 @@ __device__ __forceinline__ float stored(float x)
     return (float)(_Float16)x;
 }
 
-// Eight elements from p + j: `cnt` of them exist (the rest read as 0).
-template <int DT>
-__device__ __forceinline__ void load8(const void *p, int64_t j, int cnt, float v[8])
+// Eight elements from p + j: `cnt` of them exist (the rest read as 0).  EIGHTS:
+// cnt is 0 or 8, as where rows are a multiple of eight long; the code for
+// single elements, and the registers it keeps apart, fall away.
+template <int DT, bool EIGHTS = false>
+__device__ __forceinline__ Raw<DT> load_raw(const void *p, int64_t j, int cnt)
 {
     typedef typename Elem<DT>::T T;
     const T *q = (const T *)p + j;
-    if (cnt >= 8) {
-        if (DT == kP32) {
-            const u4_any a = gld<u4_any>(q), b = gld<u4_any>(q + 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) { v[i] = bitsf(a[i]); v[4 + i] = bitsf(b[i]); }
-        } else {
-            const u4_any a = gld<u4_any>(q);
-            const uint32_t w[4] = {a[0], a[1], a[2], a[3]};
-            unpack8<DT>(w, v);
+    Raw<DT> r;
+    if (EIGHTS) {
+        r.v[0] = r.v[DT == kP32] = (u4){0, 0, 0, 0};
+        if (cnt > 0) {
+            r.v[0] = gld<u4_any>(q);
+            if (DT == kP32) r.v[DT == kP32] = gld<u4_any>(q + 4);
         }
-        return;
+        return r;
     }
+    if (cnt >= 8) {
+        r.v[0] = gld<u4_any>(q);
+        if (DT == kP32) r.v[DT == kP32] = gld<u4_any>(q + 4);
+        return r;
+    }
+    uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        v[i] = 0.0f;
-        if (i < cnt) {
-            if (DT == kP32) v[i] = gld<float>(q + i);
-            else if (DT == kPBF16) v[i] = bf16_lo(gld<uint16_t>(q + i));
-            else v[i] = f16_lo(gld<uint16_t>(q + i));
-        }
+        w[i] = 0;
+        if (i < cnt) w[i] = DT == kP32 ? gld<uint32_t>(q + i) : gld<uint16_t>(q + i);
     }
+    if (DT == kP32) {
+        r.v[0] = (u4){w[0], w[1], w[2], w[3]};
+        r.v[DT == kP32] = (u4){w[4], w[5], w[6], w[7]};
+    } else {
+        r.v[0] = (u4){w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
+    }
+    return r;
 }
 
 template <int DT>
+__device__ __forceinline__ void unpack_raw(const Raw<DT> &r, float v[8])
+{
+    if (DT == kP32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = bitsf(r.v[i >> 2 & (DT == kP32)][i & 3]);
+    } else {
+        const uint32_t w[4] = {r.v[0][0], r.v[0][1], r.v[0][2], r.v[0][3]};
+        unpack8<DT>(w, v);
+    }
+}
+
+template <int DT, bool EIGHTS = false>
+__device__ __forceinline__ void load8(const void *p, int64_t j, int cnt, float v[8])
+{
+    unpack_raw<DT>(load_raw<DT, EIGHTS>(p, j, cnt), v);
+}
+
+template <int DT, bool EIGHTS = false>
 __device__ __forceinline__ void store8(void *p, int64_t j, int cnt, const float v[8])
 {
     typedef typename Elem<DT>::T T;
@@ -151,6 +180,7 @@ __device__ __forceinline__ void store8(void *p, int64_t j, int cnt, const float 
         }
         return;
     }
+    if (EIGHTS) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         if (i < cnt) {
@@ -161,11 +191,12 @@ __device__ __forceinline__ void store8(void *p, int64_t j, int cnt, const float 
 }
 
 // The same from a matrix whose element type is known at run time (weights).
+template <bool EIGHTS>
 __device__ __forceinline__ void load8_any(int dt, const void *p, int64_t j, int cnt, float v[8])
 {
-    if (dt == kP32) load8<kP32>(p, j, cnt, v);
-    else if (dt == kPBF16) load8<kPBF16>(p, j, cnt, v);
-    else load8<kPF16>(p, j, cnt, v);
+    if (dt == kP32) load8<kP32, EIGHTS>(p, j, cnt, v);
+    else if (dt == kPBF16) load8<kPBF16, EIGHTS>(p, j, cnt, v);
+    else load8<kPF16, EIGHTS>(p, j, cnt, v);
 }
 
 __device__ __forceinline__ int left8(int64_t j, int64_t end) { return end - j >= 8 ? 8 : end > j ? (int)(end - j) : 0; }
