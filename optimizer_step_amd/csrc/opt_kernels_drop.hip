@@ -27,8 +27,8 @@ __global__ __launch_bounds__(kDropThreads) void dropout_kernel(DropArgs a)
         for (int u = 0; u < kDropGroups; ++u) {
             const int64_t g = g0 + u * kDropThreads;
             const int cnt = left8(8 * g, a.n);
-            load8<DT>(a.x, 8 * g, cnt, x[u]);
-            if (RES) load8<DT>(a.res, 8 * g, cnt, r[u]);
+            load8<DT, false, true>(a.x, 8 * g, cnt, x[u]);
+            if (RES) load8<DT, false, true>(a.res, 8 * g, cnt, r[u]);
         }
 #pragma unroll
         for (int u = 0; u < kDropGroups; ++u) {
@@ -45,7 +45,7 @@ __global__ __launch_bounds__(kDropThreads) void dropout_kernel(DropArgs a)
                 v[i] = bits >= a.threshold ? x[u][i] * a.scale : 0.0f;
                 if (RES) v[i] = v[i] + r[u][i];
             }
-            store8<DT>(a.out, 8 * g, left8(8 * g, a.n), v);
+            store8<DT, false, true>(a.out, 8 * g, left8(8 * g, a.n), v);
         }
     }
 }

@@ -52,7 +52,7 @@ __device__ __forceinline__ double lanes_sum(double x)
 
 // 1/sqrt(x) to within 2^-51: the hardware's estimate and two Newton steps, a
 // tenth of the instructions of a division after a square root (each of which
-// every wave would run once a row: 33 -> 29 us of a pass over 8192 x 4096).
+// every wave would run once a row: 33 -> 31 us of a pass over 8192 x 4096).
 // Where a step has no value (x zero or infinite) the estimate is the result.
 __device__ __forceinline__ double inverse_root(double x)
 {
@@ -89,6 +89,9 @@ __device__ __forceinline__ void row_sums(double (&v)[N], double (*slot)[N])
     }
 }
 
+// h stays in its stored form between the sum and the result: for 16-bit types
+// half the registers.  Stores carry the non-temporal hint: 51 -> 46 us at
+// 8192 x 4096 bf16 with a residual and codes; on the loads it costs as much.
 template <int DT, int LANES, int VECS, bool EIGHTS>
 __global__ __launch_bounds__(norm_threads(LANES)) void rms_norm_kernel(NormArgs a)
 {
@@ -99,38 +102,38 @@ __global__ __launch_bounds__(norm_threads(LANES)) void rms_norm_kernel(NormArgs 
     for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.rows; r0 += (int64_t)gridDim.x * kRows, turn ^= 1) {
         const int64_t row = r0 + threadIdx.x / LANES;
         const bool live = row < a.rows;
-        constexpr bool kEarly = VECS <= 2;      // the weight waits in registers where there are some
-        float h[VECS][8], w[kEarly ? VECS : 1][8];
+        Raw<DT> h[VECS];
         double ss[1] = {0.0};
 #pragma unroll
         for (int j = 0; j < VECS; ++j) {
             const int64_t c = 8 * (int64_t)(lane + j * LANES);
-            load8<DT, EIGHTS>(a.x, row * a.ldx + c, live ? left8(c, a.cols) : 0, h[j]);
+            h[j] = load_raw<DT, EIGHTS>(a.x, row * a.ldx + c, live ? left8(c, a.cols) : 0);
         }
         if (a.res) {
-            float t[VECS][8];
+            Raw<DT> t[VECS];
 #pragma unroll
             for (int j = 0; j < VECS; ++j) {
                 const int64_t c = 8 * (int64_t)(lane + j * LANES);
-                load8<DT, EIGHTS>(a.res, row * a.ldr + c, live ? left8(c, a.cols) : 0, t[j]);
+                t[j] = load_raw<DT, EIGHTS>(a.res, row * a.ldr + c, live ? left8(c, a.cols) : 0);
             }
 #pragma unroll
-            for (int j = 0; j < VECS; ++j)
+            for (int j = 0; j < VECS; ++j) {
+                float u[8], v[8];
+                unpack_raw<DT>(h[j], u);
+                unpack_raw<DT>(t[j], v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) h[j][i] = stored<DT>(h[j][i] + t[j][i]);
+                for (int i = 0; i < 8; ++i) u[i] = u[i] + v[i];
+                h[j] = pack_raw<DT>(u);
+            }
         }
-        if (kEarly)
-#pragma unroll
-            for (int j = 0; j < VECS; ++j) {
-                const int64_t c = 8 * (int64_t)(lane + j * LANES);
-                load8_any<EIGHTS>(a.w_dtype, a.w, c, left8(c, a.cols), w[j * kEarly]);
-            }
 #pragma unroll
         for (int j = 0; j < VECS; ++j) {
             const int64_t c = 8 * (int64_t)(lane + j * LANES);
-            if (a.h) store8<DT, EIGHTS>(a.h, row * a.ldh + c, live ? left8(c, a.cols) : 0, h[j]);
+            if (a.h) store_raw<DT, EIGHTS, true>(a.h, row * a.ldh + c, live ? left8(c, a.cols) : 0, h[j]);
+            float u[8];
+            unpack_raw<DT>(h[j], u);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss[0] = __builtin_fma((double)h[j][i], (double)h[j][i], ss[0]);
+            for (int i = 0; i < 8; ++i) ss[0] = __builtin_fma((double)u[i], (double)u[i], ss[0]);
         }
         row_sums<LANES, 1>(ss, slot[turn]);
         const float r = (float)inverse_root(__builtin_fma(ss[0], a.inv_cols, a.eps));
@@ -138,15 +141,16 @@ __global__ __launch_bounds__(norm_threads(LANES)) void rms_norm_kernel(NormArgs 
         for (int j = 0; j < VECS; ++j) {
             const int64_t c = 8 * (int64_t)(lane + j * LANES);
             const int cnt = live ? left8(c, a.cols) : 0;
-            float y[8];
-            if (!kEarly) load8_any<EIGHTS>(a.w_dtype, a.w, c, left8(c, a.cols), w[0]);
+            float w[8], u[8], y[8];
+            load8_any<EIGHTS>(a.w_dtype, a.w, c, left8(c, a.cols), w);
+            unpack_raw<DT>(h[j], u);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = i < cnt ? (h[j][i] * r) * w[j * kEarly][i] : 0.0f;
-            if (a.y) store8<DT, EIGHTS>(a.y, row * a.ldy + c, cnt, y);
+            for (int i = 0; i < 8; ++i) y[i] = i < cnt ? (u[i] * r) * w[i] : 0.0f;
+            if (a.y) store8<DT, EIGHTS, true>(a.y, row * a.ldy + c, cnt, y);
             if (a.q.codes) {
                 const uint32_t byte = block_scale(row16_max_u32(abs_max8(y)));
                 const u2 code = encode8(y, byte);
-                if (live && c < ((a.cols + 15) & ~(int64_t)15)) gst<u2>(a.q.codes + row * a.q.ld + c, code);
+                if (live && c < ((a.cols + 15) & ~(int64_t)15)) sst<u2>(a.q.codes + row * a.q.ld + c, code);
                 if (cnt > 0 && (lane & 15) == 0) gst<uint8_t>(a.q.scales + (c / kCodeBlock) * a.q.lds + row, (uint8_t)byte);
             }
         }
@@ -182,27 +186,31 @@ __global__ __launch_bounds__(norm_threads(LANES)) void rms_norm_grad_kernel(Norm
     __shared__ float comb[LANES < 256 ? 256 * 8 : 1];
     const int lane = threadIdx.x % LANES;
     const int64_t step = (int64_t)gridDim.x * kRows;
-    float dw[VECS][8] = {};
-    int turn = 0;
-    int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / LANES;
-    GradRow<DT, VECS> g, next;
-    load_row<DT, LANES, VECS, EIGHTS>(a, row, g);
-    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.rows; r0 += step, row += step, turn ^= 1) {
+    constexpr bool kKeep = VECS <= 2;           // the weight stays in registers
+    float dw[VECS][8] = {}, w[kKeep ? VECS : 1][8];
+    if (kKeep)
+#pragma unroll
+        for (int j = 0; j < VECS; ++j) {
+            const int64_t c = 8 * (int64_t)(lane + j * LANES);
+            load8_any<EIGHTS>(a.w_dtype, a.w, c, left8(c, a.cols), w[j * kKeep]);
+        }
+    // one row (or group of rows); `g` holds it, `next` takes the one after it
+    auto one = [&](int64_t row, GradRow<DT, VECS> &g, GradRow<DT, VECS> &next, int turn) {
         const bool live = row < a.rows;
         if (kAhead) load_row<DT, LANES, VECS, EIGHTS>(a, row + step, next);
-        else if (turn || r0 >= step) load_row<DT, LANES, VECS, EIGHTS>(a, row, g);
         double s[2] = {0.0, 0.0};
 #pragma unroll
         for (int j = 0; j < VECS; ++j) {
             const int64_t c = 8 * (int64_t)(lane + j * LANES);
-            float w[8], h[8], dy[8];
-            load8_any<EIGHTS>(a.w_dtype, a.w, c, left8(c, a.cols), w);
+            float h[8], dy[8];
+            if (!kKeep) load8_any<EIGHTS>(a.w_dtype, a.w, c, left8(c, a.cols), w[0]);
             unpack_raw<DT>(g.h[j], h);
             unpack_raw<DT>(g.dy[j], dy);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                s[0] = __builtin_fma((double)h[i], (double)h[i], s[0]);
-                s[1] = __builtin_fma((double)(dy[i] * w[i]), (double)h[i], s[1]);
+                const double hd = (double)h[i];
+                s[0] = __builtin_fma(hd, hd, s[0]);
+                s[1] = __builtin_fma((double)(dy[i] * w[j * kKeep][i]), hd, s[1]);
             }
         }
         row_sums<LANES, 2>(s, slot[turn]);
@@ -212,13 +220,13 @@ __global__ __launch_bounds__(norm_threads(LANES)) void rms_norm_grad_kernel(Norm
         for (int j = 0; j < VECS; ++j) {
             const int64_t c = 8 * (int64_t)(lane + j * LANES);
             const int cnt = live ? left8(c, a.cols) : 0;
-            float w[8], h[8], dy[8], dx[8];
-            load8_any<EIGHTS>(a.w_dtype, a.w, c, left8(c, a.cols), w);
+            float h[8], dy[8], dx[8];
+            if (!kKeep) load8_any<EIGHTS>(a.w_dtype, a.w, c, left8(c, a.cols), w[0]);
             unpack_raw<DT>(g.h[j], h);
             unpack_raw<DT>(g.dy[j], dy);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                dx[i] = r * (dy[i] * w[i] - h[i] * k);
+                dx[i] = r * (dy[i] * w[j * kKeep][i] - h[i] * k);
                 if (live) dw[j][i] += dy[i] * (h[i] * r);
             }
             if (a.dh) {
@@ -227,9 +235,22 @@ __global__ __launch_bounds__(norm_threads(LANES)) void rms_norm_grad_kernel(Norm
 #pragma unroll
                 for (int i = 0; i < 8; ++i) dx[i] = dx[i] + t[i];
             }
-            store8<DT, EIGHTS>(a.dx, row * a.lddx + c, cnt, dx);
+            store8<DT, EIGHTS, true>(a.dx, row * a.lddx + c, cnt, dx);
         }
-        if (kAhead) g = next;
+    };
+    int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / LANES, r0 = (int64_t)blockIdx.x * kRows;
+    GradRow<DT, VECS> g0, g1;
+    load_row<DT, LANES, VECS, EIGHTS>(a, row, g0);
+    while (r0 < a.rows) {
+        one(row, g0, g1, 0);
+        row += step;
+        r0 += step;
+        if (r0 >= a.rows) break;
+        if (!kAhead) load_row<DT, LANES, VECS, EIGHTS>(a, row, g0);
+        one(row, kAhead ? g1 : g0, g0, 1);
+        row += step;
+        r0 += step;
+        if (!kAhead && r0 < a.rows) load_row<DT, LANES, VECS, EIGHTS>(a, row, g0);
     }
     if (!a.part) return;
     // the workgroup's partial sums: rows of one wave by shuffles, then waves
@@ -284,14 +305,14 @@ __global__ __launch_bounds__(1024) void norm_dw_kernel(const float *part, int64_
     }
 }
 
-#ifndef NG
-#define NG 1024
-#endif
+// A workgroup of 256 holds a row of 2048 to 8192 columns: a wave alone (no
+// barrier, 32 KB in flight) measured 54 us against 45 forward and 97 against 61
+// backward at 8192 x 4096.
 NormShape norm_shape(int64_t cols)
 {
     const int64_t v = (cols + 7) / 8;                 // groups of eight in a row
     NormShape s;
-    s.lanes = v <= 64 ? 16 : v <= 256 ? 64 : v <= 2048 ? 256 : 1024;
+    s.lanes = v <= 64 ? 16 : v <= 256 ? 64 : v <= 1024 ? 256 : 1024;
     s.vecs = 1;
     while ((int64_t)s.lanes * s.vecs < v) s.vecs *= 2;
     return s;
@@ -302,11 +323,11 @@ int64_t norm_grad_groups(int64_t rows, int64_t cols)
     const NormShape s = norm_shape(cols);
     const int64_t per = s.lanes < 256 ? 256 / s.lanes : 1;
     const int64_t n = (rows + per - 1) / per;
-    const int64_t most = s.lanes == 1024 ? 256 : NG;
+    const int64_t most = s.lanes == 1024 ? 256 : 512;   // two workgroups a compute unit; 768 measured 57.3 us, 1024 61.5 against 55.5
     return n < most ? n : most;
 }
 
-#define NORM_SHAPES(X) X(16, 1) X(16, 2) X(16, 4) X(64, 2) X(64, 4) X(256, 2) X(256, 4) X(256, 8) X(1024, 4)
+#define NORM_SHAPES(X) X(16, 1) X(16, 2) X(16, 4) X(64, 2) X(64, 4) X(256, 2) X(256, 4) X(1024, 2) X(1024, 4)
 
 template <int DT>
 static hipError_t launch_norm_t(const NormArgs &a, hipStream_t st)

@@ -102,19 +102,25 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     return f16_rne(a) | (f16_rne(b) << 16);
 }
 
-// The value a stored element reads back as.
-template <int DT>
-__device__ __forceinline__ float stored(float x)
+// NT: the non-temporal hint, where a kernel's comment gives its measure.
+template <bool NT>
+__device__ __forceinline__ u4 any16(const void *p)
 {
-    if (DT == kP32) return x;
-    if (DT == kPBF16) return bf16_lo(bf16x2_rne(x, 0.0f));
-    return (float)(_Float16)x;
+    if (NT) return sld<u4_any>(p);
+    return gld<u4_any>(p);
+}
+
+template <bool NT>
+__device__ __forceinline__ void put16(void *p, u4 v)
+{
+    if (NT) sst<u4_any>(p, v);
+    else gst<u4_any>(p, v);
 }
 
 // Eight elements from p + j: `cnt` of them exist (the rest read as 0).  EIGHTS:
 // cnt is 0 or 8, as where rows are a multiple of eight long; the code for
 // single elements, and the registers it keeps apart, fall away.
-template <int DT, bool EIGHTS = false>
+template <int DT, bool EIGHTS = false, bool NT = false>
 __device__ __forceinline__ Raw<DT> load_raw(const void *p, int64_t j, int cnt)
 {
     typedef typename Elem<DT>::T T;
@@ -123,14 +129,14 @@ __device__ __forceinline__ Raw<DT> load_raw(const void *p, int64_t j, int cnt)
     if (EIGHTS) {
         r.v[0] = r.v[DT == kP32] = (u4){0, 0, 0, 0};
         if (cnt > 0) {
-            r.v[0] = gld<u4_any>(q);
-            if (DT == kP32) r.v[DT == kP32] = gld<u4_any>(q + 4);
+            r.v[0] = any16<NT>(q);
+            if (DT == kP32) r.v[DT == kP32] = any16<NT>(q + 4);
         }
         return r;
     }
     if (cnt >= 8) {
-        r.v[0] = gld<u4_any>(q);
-        if (DT == kP32) r.v[DT == kP32] = gld<u4_any>(q + 4);
+        r.v[0] = any16<NT>(q);
+        if (DT == kP32) r.v[DT == kP32] = any16<NT>(q + 4);
         return r;
     }
     uint32_t w[8];
@@ -160,34 +166,50 @@ __device__ __forceinline__ void unpack_raw(const Raw<DT> &r, float v[8])
     }
 }
 
-template <int DT, bool EIGHTS = false>
-__device__ __forceinline__ void load8(const void *p, int64_t j, int cnt, float v[8])
+// Eight values as they are stored, rounded to nearest-even.
+template <int DT>
+__device__ __forceinline__ Raw<DT> pack_raw(const float v[8])
 {
-    unpack_raw<DT>(load_raw<DT, EIGHTS>(p, j, cnt), v);
+    Raw<DT> r;
+    if (DT == kP32) {
+        r.v[0] = (u4){fbits(v[0]), fbits(v[1]), fbits(v[2]), fbits(v[3])};
+        r.v[DT == kP32] = (u4){fbits(v[4]), fbits(v[5]), fbits(v[6]), fbits(v[7])};
+    } else {
+        r.v[0] = (u4){pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])};
+    }
+    return r;
 }
 
-template <int DT, bool EIGHTS = false>
-__device__ __forceinline__ void store8(void *p, int64_t j, int cnt, const float v[8])
+template <int DT, bool EIGHTS = false, bool NT = false>
+__device__ __forceinline__ void load8(const void *p, int64_t j, int cnt, float v[8])
+{
+    unpack_raw<DT>(load_raw<DT, EIGHTS, NT>(p, j, cnt), v);
+}
+
+template <int DT, bool EIGHTS = false, bool NT = false>
+__device__ __forceinline__ void store_raw(void *p, int64_t j, int cnt, const Raw<DT> &r)
 {
     typedef typename Elem<DT>::T T;
     T *q = (T *)p + j;
     if (cnt >= 8) {
-        if (DT == kP32) {
-            gst<u4_any>(q, (u4_any){fbits(v[0]), fbits(v[1]), fbits(v[2]), fbits(v[3])});
-            gst<u4_any>(q + 4, (u4_any){fbits(v[4]), fbits(v[5]), fbits(v[6]), fbits(v[7])});
-        } else {
-            gst<u4_any>(q, (u4_any){pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])});
-        }
+        put16<NT>(q, r.v[0]);
+        if (DT == kP32) put16<NT>(q + 4, r.v[DT == kP32]);
         return;
     }
     if (EIGHTS) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         if (i < cnt) {
-            if (DT == kP32) gst<float>(q + i, v[i]);
-            else gst<uint16_t>(q + i, (uint16_t)(pack2<DT>(v[i], 0.0f) & 0xFFFFu));
+            if (DT == kP32) gst<uint32_t>(q + i, r.v[i >> 2 & (DT == kP32)][i & 3]);
+            else gst<uint16_t>(q + i, (uint16_t)(r.v[0][i >> 1] >> (16 * (i & 1))));
         }
     }
+}
+
+template <int DT, bool EIGHTS = false, bool NT = false>
+__device__ __forceinline__ void store8(void *p, int64_t j, int cnt, const float v[8])
+{
+    store_raw<DT, EIGHTS, NT>(p, j, cnt, pack_raw<DT>(v));
 }
 
 // The same from a matrix whose element type is known at run time (weights).
