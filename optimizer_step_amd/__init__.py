@@ -531,8 +531,8 @@ def _coded(pair, what, rows, cols, dev):
     if (qc > 1 and qs != 1) or (sc > 1 and ss != 1):
         raise ValueError(f"{what} codes and scales must have contiguous rows")
     width, height = (cols + 15) // 16 * 16, (rows + 3) // 4 * 4
-    if qr != rows or qc < width:
-        raise ValueError(f"{what} codes must be [{rows}, >= {width}], got {list(q.shape)}")
+    if qr != rows or qc != width:
+        raise ValueError(f"{what} codes must be [{rows}, {width}], got {list(q.shape)}")
     if sr < (cols + CODE_BLOCK - 1) // CODE_BLOCK or sc < height:
         raise ValueError(f"{what} scales must be [>= {(cols + CODE_BLOCK - 1) // CODE_BLOCK}, >= {height}], got {list(s.shape)}")
     return OptCodes(q.data_ptr(), ql if rows > 1 else width, s.data_ptr(), sl if sr > 1 else height)

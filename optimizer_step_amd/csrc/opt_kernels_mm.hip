@@ -82,8 +82,9 @@ __device__ __forceinline__ void store_c(const MatmulArgs &a, int64_t m, int64_t 
 
 // A workgroup of four waves forms 16 x MT rows of A by 16 of B; each wave sums
 // every fourth block of 128 columns and the four sums meet in LDS.  It is bound
-// by the read of B: a wave has the pieces of kAhead blocks in flight.
-constexpr int kAhead = 4;
+// by the read of B, at 3 to 4 TB/s: a wave has the pieces of four or eight
+// blocks in flight (one row by 32000 x 4096: 33 to 36 us with eight, 38 with four;
+// the non-temporal hint on B lost 10-30 %).
 
 template <int MT, int U, bool WHOLE>
 __device__ __forceinline__ void rows_blocks(const MatmulArgs &a, f4 (&acc)[MT], int64_t nr, const int64_t (&mr)[MT], int64_t block,
@@ -127,7 +128,9 @@ __global__ __launch_bounds__(256) void product_rows_kernel(MatmulArgs a)
             acc[i] = (f4){0, 0, 0, 0};
         }
         int64_t block = wave;
-        for (; block + 4 * (kAhead - 1) < whole; block += 4 * kAhead) rows_blocks<MT, kAhead, true>(a, acc, nr, mr, block, part);
+        if (MT == 1)
+            for (; block + 28 < whole; block += 32) rows_blocks<MT, 8, true>(a, acc, nr, mr, block, part);
+        for (; block + 12 < whole; block += 16) rows_blocks<MT, 4, true>(a, acc, nr, mr, block, part);
         for (; block < blocks; block += 4) rows_blocks<MT, 1, false>(a, acc, nr, mr, block, part);
         __syncthreads();
         if (wave > 0)
@@ -196,15 +199,19 @@ struct StageCopy {
     // Column (byte) of a row at which this thread's pieces start.
     __device__ __forceinline__ int column() const { return 16 * ((threadIdx.x & 7) ^ ((threadIdx.x >> 4) & 7)); }
 
-    // Rows past the last are outside the buffer that the loads are given: what
-    // their part of LDS then holds goes into rows of C that are not stored.
+    // Rows past the last lie outside the buffer that the loads are given (its
+    // bounds check takes the lane's offset, not the scalar one, so the row is
+    // in the lane's): nothing is read there, and what their part of LDS then
+    // holds goes into rows of C that are not stored.
     __device__ __forceinline__ void copy(int k0, uint8_t *lds, int from = 0, int to = kCopies) const
     {
         const auto src = __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, rows * ld, 0x00027000);
+        int at = first;
+        asm volatile("" : "+v"(at));       // the sums below are formed each time: held, they would not fit the registers
 #pragma unroll
         for (int i = from; i < to; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (OPT_LDS void *)(lds + 16 * (i * THREADS) + wave_at), 16,
-                                                     first, k0 + lds_row_source<T>(i * kStep) * ld, 0, 0);
+                                                     at + lds_row_source<T>(i * kStep) * ld, k0, 0, 0);
     }
     // the last stage of rows that end inside it: pieces past the end are zeros
     __device__ __forceinline__ void copy_tail(int k0, uint8_t *lds, int left) const
