@@ -1,6 +1,14 @@
 // opt_kernels_cast.hip -- the cast to block-coded matrices: E4M3 codes with
-// one power-of-two scale for each row (or each 128 rows) and 128 columns, of
+// one power-of-two scale X for each row (or each 128 rows) and 128 columns, of
 // the matrix and/or of its transpose, in one read of it.
+//
+// X is the smallest power of two with A <= 448 X (A the block's largest
+// magnitude): x / X is exact and never leaves the grid, so a code is one
+// conversion.  The tile is 128 x 128 because the transpose's blocks are 128
+// rows tall: both layouts' maxima and codes come from one read.  Bound by HBM
+// on the way in and out: both layouts of 8192 x 4096 bf16 take 28.3 us (134 MB,
+// 4.7 TB/s), one layout 20 to 22 us, a 11008 x 4096 fp32 weight 51.8 us (271 MB,
+// 5.2 TB/s); the vector units are busy 41 and 21 % of the time.
 #include "opt_pass.h"
 
 namespace optstep {
@@ -44,7 +52,7 @@ __device__ __forceinline__ float raw_at(const Raw<DT> &r, int k)
 // One 128 x 128 tile a workgroup.  Thread t holds the eight columns of group
 // t % 16 in the eight rows of group t / 16: a row's block maximum is one DPP
 // row, a column's codes of eight rows are one 8-byte LDS store.
-template <int DT, bool SQUARE, bool EIGHTS>
+template <int DT, bool SQUARE>
 __global__ __launch_bounds__(256) void block_cast_kernel(CastArgs a)
 {
     __shared__ uint32_t cmax[4][128];
@@ -58,7 +66,7 @@ __global__ __launch_bounds__(256) void block_cast_kernel(CastArgs a)
         Raw<DT> x[8];
         // the matrix is read once: the non-temporal hint, 57 -> 53 us at 11008 x 4096 fp32
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = load_raw<DT, EIGHTS, true>(a.x, (r + i) * a.ldx + c, i < live ? cnt : 0);
+        for (int i = 0; i < 8; ++i) x[i] = load_raw<DT, false, true>(a.x, (r + i) * a.ldx + c, i < live ? cnt : 0);
         uint32_t rm[8], cm[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) cm[k] = 0;
@@ -147,11 +155,8 @@ static hipError_t launch_cast_t(const CastArgs &a, int square, hipStream_t st)
 {
     const int64_t tiles = ((a.cols + 127) / 128) * ((a.rows + 127) / 128);
     const unsigned grid = (unsigned)(tiles < (1 << 20) ? tiles : 1 << 20);
-    const bool eights = a.cols % 8 == 0;
-    if (square && eights) hipLaunchKernelGGL((block_cast_kernel<DT, true, true>), dim3(grid), dim3(256), 0, st, a);
-    else if (square) hipLaunchKernelGGL((block_cast_kernel<DT, true, false>), dim3(grid), dim3(256), 0, st, a);
-    else if (eights) hipLaunchKernelGGL((block_cast_kernel<DT, false, true>), dim3(grid), dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((block_cast_kernel<DT, false, false>), dim3(grid), dim3(256), 0, st, a);
+    if (square) hipLaunchKernelGGL((block_cast_kernel<DT, true>), dim3(grid), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((block_cast_kernel<DT, false>), dim3(grid), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 

@@ -3,6 +3,12 @@
 // out_j = res_j + (r_j >= T ? x_j * s : 0), with r_j the 16 bits of element j
 // in its stream; the mask is recomputed wherever it is needed and never
 // stored, so the backward pass is the same kernel on the gradient.
+//
+// Bound by HBM: 8192 x 4096 bf16 with a residual takes 32.3 us (201 MB, 6.2
+// TB/s).  Sixteen bits an element keep the generator below that: one block of
+// it, about 160 issue cycles, serves eight elements, and the vector units are
+// busy 32 % of the time; p is then a multiple of 2^-16.  Loads and stores carry
+// the non-temporal hint (37.6 us without).
 #include "opt_pass.h"
 
 namespace optstep {

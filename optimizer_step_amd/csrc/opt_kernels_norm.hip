@@ -6,8 +6,10 @@
 // y = fl(fl(h * r) * w).  Backward:  g = dy * w,  c = mean(g * h),
 // dx = r * (g - h * (r^2 c)) [+ dh],  dw = sum over rows of dy * (h * r).
 //
-// Both are bound by HBM: every matrix crosses it once.  A row stays in the
-// registers of `LANES` lanes, eight consecutive elements (16 bytes of 16-bit
+// Both are bound by HBM: every matrix crosses it once (8192 x 4096 bf16: with
+// the residual and codes 45 us for 237 MB, 5.2 TB/s; backward with the
+// residual's gradient 55.5 us for 268 MB, of which the weight's gradient 5).
+// A row stays in the registers of `LANES` lanes, eight consecutive elements (16 bytes of 16-bit
 // words) a lane at a time, so that a 128-column block is one 16-lane DPP row
 // and its largest magnitude takes four DPP steps.  Squares are summed in
 // binary64, whose rate is half of binary32's here and leaves the kernel bound
@@ -89,6 +91,9 @@ __device__ __forceinline__ void row_sums(double (&v)[N], double (*slot)[N])
     }
 }
 
+// EIGHTS: rows of a multiple of eight elements, without the code for single
+// ones (8192 x 4096 bf16 to codes 25.2 us, with it 26.9).
+//
 // h stays in its stored form between the sum and the result: for 16-bit types
 // half the registers.  Stores carry the non-temporal hint: 51 -> 46 us at
 // 8192 x 4096 bf16 with a residual and codes; on the loads it costs as much.

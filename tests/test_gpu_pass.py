@@ -685,19 +685,20 @@ def test_captured_layers():
         assert all(torch.equal(a[k], b[k]) for k in OUTPUTS)
 
 
-def test_product_small_scales():
+@pytest.mark.parametrize("m,n,dtype", [(4, 16, "f32"), (4, 16, "bf16"), (300, 2600, "f32"), (300, 2600, "bf16")])
+def test_product_small_scales(m, n, dtype):
     """The smallest scale, on a block of tiny values against large ones."""
     import torch
     import optimizer_step_amd as osa
-    a, b = osa.block_buffers(4, 256), osa.block_buffers(16, 256)
-    x = np.ones((4, 256), np.float32)
+    a, b = osa.block_buffers(m, 256), osa.block_buffers(n, 256)
+    x = np.ones((m, 256), np.float32)
     x[:, :128] = 1.5 * 2.0 ** -119
     osa.opt_block_cast(dev(x, "f32"), codes=a)
-    osa.opt_block_cast(torch.full((16, 256), 2.0 ** 100, device="cuda"), codes=b)
+    osa.opt_block_cast(torch.full((n, 256), 2.0 ** 100, device="cuda"), codes=b)
     assert int(a[1][0, 0]) == 0
-    c = empty(4, 16, "f32")
+    c = empty(m, n, dtype)
     osa.opt_block_matmul(a, b, c)
     want = 128 * 2.0 ** 100 * (1 + 1.5 * 2.0 ** -119)
-    assert np.array_equal(host(c), np.full((4, 16), want, np.float32))
+    assert np.array_equal(host(c), np.full((m, n), want, np.float32))
     osa.opt_block_matmul((a[0][:, :128], a[1]), (b[0][:, :128], b[1]), c)
-    assert np.array_equal(host(c), np.full((4, 16), 1.5 * 128 * 2.0 ** -19, np.float32))
+    assert np.array_equal(host(c), np.full((m, n), 1.5 * 128 * 2.0 ** -19, np.float32))
