@@ -486,6 +486,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(MatmulArgs a
             half.step(acc, fa, fb0, sa, sb, fb0, sa, sb, [](int) {}, [&](int i) { return la_row.read(la0, min(i + PF, TM - 1), z); });
         }
     }
+    __builtin_amdgcn_s_waitcnt(0x0F70);     // vmcnt(0): no copy is on its way when the workgroup gives its LDS up
     // lane (r, h) holds rows TM r + i of C and, of the columns TN x + j, those
     // with x = 8 g + 4 h + e: 4 TN neighbouring ones for each g
 #pragma unroll
