@@ -3,7 +3,9 @@
  * optimizer step: AdamW and AdEMAMix with decoupled weight decay applied in
  * the decay-first order, optimizer states stored as fp32, BF16 (nearest or
  * stochastic rounding) or 8-bit blockwise codes, and a deterministic
- * update-norm pre-pass for max_unorm.
+ * update-norm pre-pass for max_unorm.  Beside it: gradient norms, a rounding
+ * cast, and the operators of a training pass that form the step's gradients
+ * (dropout, RMS norm, block-coded 8-bit matrices and their product).
  *
  * The operation (sources are the four pages this library is built from):
  *  - decay-first AdamW, p' = p*(1 - lr*wd) - lr*u with u = m_hat/(sqrt(v_hat)+eps):

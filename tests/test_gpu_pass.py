@@ -702,3 +702,29 @@ def test_product_small_scales(m, n, dtype):
     assert np.array_equal(host(c), np.full((m, n), want, np.float32))
     osa.opt_block_matmul((a[0][:, :128], a[1]), (b[0][:, :128], b[1]), c)
     assert np.array_equal(host(c), np.full((m, n), 1.5 * 128 * 2.0 ** -19, np.float32))
+
+
+def test_readme_layer_runs():
+    """The layer example of README.md runs as written; its weight gradient and
+    dx against the pass in binary32 from the tensors it holds."""
+    import os
+    import re
+    import torch
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    code = re.findall(r"```python\n(.*?)```", text, re.S)[1]
+    torch.manual_seed(0)
+    env = {}
+    exec(compile("import torch, optimizer_step_amd as osa\n" + code, "README.md", "exec"), env)
+    torch.cuda.synchronize()
+
+    def decoded(pair, rows, cols):
+        return torch.from_numpy(P.decode(pair[0].cpu().numpy(), pair[1].cpu().numpy()[:, :rows], cols)).float().cuda()
+
+    tokens, inner, outer = env["tokens"], env["inner"], env["outer"]
+    want = decoded(env["zt"], outer, tokens) @ decoded(env["yt"], inner, tokens).t()
+    # both sums in binary32: each off by (k + 8) * 2^-23 of the sum of magnitudes
+    # at most; on random data that is far inside 2^-23 * k of the result's norm
+    assert float((env["dweight"] - want).norm() / want.norm()) <= tokens * 2.0 ** -23
+    keep = P.random_bits(4096, 7, 1) >= round(0.1 * 65536)
+    first = env["dx"].view(-1)[:4096].float().cpu().numpy()
+    assert not first[~keep].any() and (first[keep] != 0).mean() > 0.99
