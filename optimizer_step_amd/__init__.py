@@ -491,6 +491,24 @@ def _device():
     return torch.cuda.current_device()
 
 
+_codes_of = {}
+
+
+def _type(t):
+    """_dtype_code, by a table that the first call fills."""
+    c = _codes_of.get(t.dtype)
+    if c is None:
+        c = _codes_of[t.dtype] = _dtype_code(t)
+    return c
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
+
+
 def _sides(t, what):
     """(rows, cols, leading dimension) of a matrix argument."""
     if t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1):
@@ -523,18 +541,22 @@ def _coded(pair, what, rows, cols, dev):
     if pair is None:
         return OptCodes()
     q, s = pair
+    width, height = (cols + 15) // 16 * 16, (rows + 3) // 4 * 4
     if q.dim() != 2 or s.dim() != 2 or q.element_size() != 1 or s.element_size() != 1:
         raise ValueError(f"{what} codes and scales must be 2-D tensors of bytes")
-    _on_device(q, f"{what} codes", dev)
-    _on_device(s, f"{what} scales", dev)
-    (qr, qc), (sr, sc), (ql, qs), (sl, ss) = q.shape, s.shape, q.stride(), s.stride()
-    if (qc > 1 and qs != 1) or (sc > 1 and ss != 1):
-        raise ValueError(f"{what} codes and scales must have contiguous rows")
-    width, height = (cols + 15) // 16 * 16, (rows + 3) // 4 * 4
+    if q.get_device() != dev or s.get_device() != dev:
+        _on_device(q, f"{what} codes", dev)
+        _on_device(s, f"{what} scales", dev)
+    (qr, qc), (sr, sc) = q.shape, s.shape
     if qr != rows or qc != width:
         raise ValueError(f"{what} codes must be [{rows}, {width}], got {list(q.shape)}")
     if sr < (cols + CODE_BLOCK - 1) // CODE_BLOCK or sc < height:
         raise ValueError(f"{what} scales must be [>= {(cols + CODE_BLOCK - 1) // CODE_BLOCK}, >= {height}], got {list(s.shape)}")
+    if q.is_contiguous() and s.is_contiguous():
+        return OptCodes(q.data_ptr(), width, s.data_ptr(), sc if sr > 1 else height)
+    (ql, qs), (sl, ss) = q.stride(), s.stride()
+    if (qc > 1 and qs != 1) or (sc > 1 and ss != 1):
+        raise ValueError(f"{what} codes and scales must have contiguous rows")
     return OptCodes(q.data_ptr(), ql if rows > 1 else width, s.data_ptr(), sl if sr > 1 else height)
 
 
@@ -551,15 +573,16 @@ def opt_dropout(x, out, p, seed=0, offset=0, residual=None, index_base=0, stream
             _on_device(t, what, dev)
             if not t.is_contiguous() or t.dtype != dtype or t.numel() != n:
                 raise ValueError(f"{what} must be contiguous, of x's type and size")
-    return _check(lib().opt_dropout(x.data_ptr(), _ptr(residual), out.data_ptr(), n, _dtype_code(x), float(p),
-                                    int(seed) & (2**64 - 1), int(offset) & (2**64 - 1), int(index_base), _stream(stream)))
+    L = _lib or lib()
+    return _check(L.opt_dropout(x.data_ptr(), _ptr(residual), out.data_ptr(), n, _type(x), float(p),
+                                    int(seed) & (2**64 - 1), int(offset) & (2**64 - 1), int(index_base), _raw_stream(stream, dev)))
 
 
 def _weight(w, cols, dev):
     _on_device(w, "weight", dev)
     if w.numel() != cols or not w.is_contiguous():
         raise ValueError(f"weight must be contiguous, of {cols} elements")
-    return w.data_ptr(), _dtype_code(w)
+    return w.data_ptr(), _type(w)
 
 
 def opt_rms_norm(x, weight, eps=1e-6, residual=None, h=None, y=None, codes=None, stream=None):
@@ -573,9 +596,9 @@ def opt_rms_norm(x, weight, eps=1e-6, residual=None, h=None, y=None, codes=None,
     pr, ldr = _like(residual, "residual", x, rows, cols, dev)
     ph, ldh = _like(h, "h", x, rows, cols, dev)
     py, ldy = _like(y, "y", x, rows, cols, dev)
-    a = OptNorm(rows, cols, _dtype_code(x), wd, x.data_ptr(), ldx, pr, ldr, pw, ph, ldh, py, ldy,
+    a = OptNorm(rows, cols, _type(x), wd, x.data_ptr(), ldx, pr, ldr, pw, ph, ldh, py, ldy,
                 _coded(codes, "codes'", rows, cols, dev), float(eps))
-    return _check(lib().opt_rms_norm(ctypes.byref(a), _stream(stream)))
+    return _check((_lib or lib()).opt_rms_norm(ctypes.byref(a), _raw_stream(stream, dev)))
 
 
 def opt_rms_norm_workspace(rows, cols):
@@ -622,9 +645,9 @@ def opt_rms_norm_backward(dy, h, weight, dx, dweight=None, eps=1e-6, dh=None, ac
             workspace = _scratch(need, stream)
         else:
             _device_buffer(workspace, 1, need, "workspace")
-    a = OptNormGrad(rows, cols, _dtype_code(dy), wd, dy.data_ptr(), lddy, ph, ldh, pw, pd, lddh, px, lddx, _ptr(dweight),
+    a = OptNormGrad(rows, cols, _type(dy), wd, dy.data_ptr(), lddy, ph, ldh, pw, pd, lddh, px, lddx, _ptr(dweight),
                     1 if accumulate else 0, 0, float(eps), _ptr(workspace) if need else None, need)
-    return _check(lib().opt_rms_norm_backward(ctypes.byref(a), _stream(stream)))
+    return _check((_lib or lib()).opt_rms_norm_backward(ctypes.byref(a), _raw_stream(stream, dev)))
 
 
 def opt_block_cast(x, codes=None, codes_t=None, block_rows=1, stream=None):
@@ -635,9 +658,9 @@ def opt_block_cast(x, codes=None, codes_t=None, block_rows=1, stream=None):
     dev = _device()
     _on_device(x, "x", dev)
     rows, cols, ldx = _sides(x, "x")
-    a = OptCast(rows, cols, x.data_ptr(), ldx, _dtype_code(x), int(block_rows), _coded(codes, "codes'", rows, cols, dev),
+    a = OptCast(rows, cols, x.data_ptr(), ldx, _type(x), int(block_rows), _coded(codes, "codes'", rows, cols, dev),
                 _coded(codes_t, "codes_t's", cols, rows, dev))
-    return _check(lib().opt_block_cast(ctypes.byref(a), _stream(stream)))
+    return _check((_lib or lib()).opt_block_cast(ctypes.byref(a), _raw_stream(stream, dev)))
 
 
 def opt_block_matmul(a, b, out, accumulate=False, stream=None):
@@ -649,9 +672,9 @@ def opt_block_matmul(a, b, out, accumulate=False, stream=None):
     k = a[0].shape[1]
     if b[0].shape[1] != k:
         raise ValueError(f"a has {k} code columns, b {b[0].shape[1]}")
-    r = OptProduct(m, n, k, _coded(a, "a's", m, k, dev), _coded(b, "b's", n, k, dev), out.data_ptr(), ldc, _dtype_code(out),
+    r = OptProduct(m, n, k, _coded(a, "a's", m, k, dev), _coded(b, "b's", n, k, dev), out.data_ptr(), ldc, _type(out),
                    1 if accumulate else 0)
-    return _check(lib().opt_block_matmul(ctypes.byref(r), _stream(stream)))
+    return _check((_lib or lib()).opt_block_matmul(ctypes.byref(r), _raw_stream(stream, dev)))
 
 
 def opt_debug_mini(elem, A, x, r, codes, decoded, stream=None):

@@ -42,7 +42,7 @@ __device__ __forceinline__ bf8v widen8(uint32_t lo, uint32_t hi, float scale)
 // block's 128 columns they are does not matter to the sum as long as A and B
 // agree: a lane takes two 16-byte pieces 64 columns apart, so each
 // quarter-wave reads 64 consecutive bytes.  WHOLE: the block lies inside the
-// row; else pieces past the row's end read as zero codes.
+// row; else what is past the row's end reads as zero codes (of scale byte 0).
 struct Piece {
     u4 lo, hi;
     uint32_t byte;
@@ -53,9 +53,10 @@ struct Piece {
         const uint8_t *p = q.codes + row * q.ld + block * 128 + 16 * part;
         const int64_t left = k - block * 128 - 16 * part;
         lo = hi = (u4){0, 0, 0, 0};
+        byte = 0;
         if (WHOLE || left > 0) lo = gld<u4>(p);
         if (WHOLE || left > 64) hi = gld<u4>(p + 64);
-        byte = gld<uint8_t>(q.scales + block * q.lds + row);
+        if (WHOLE || block * 128 < k) byte = gld<uint8_t>(q.scales + block * q.lds + row);
     }
     __device__ __forceinline__ void widen(bf8v v[4]) const
     {
@@ -89,9 +90,11 @@ __device__ __forceinline__ void store_c(const MatmulArgs &a, int64_t m, int64_t 
 
 // A workgroup of four waves forms 16 x MT rows of A by 16 of B; each wave sums
 // every fourth block of 128 columns and the four sums meet in LDS.  It is bound
-// by the read of B, at 3 to 4 TB/s: a wave has the pieces of four or eight
-// blocks in flight (one row by 32000 x 4096: 33 to 36 us with eight, 38 with four;
-// the non-temporal hint on B lost 10-30 %).
+// by the read of B, at 3 to 4 TB/s: a wave has the pieces of two blocks in
+// flight, of eight where 16 rows of A leave the registers for them (one row by
+// 32000 x 4096: 34 us, 38 with four; with 32 rows four blocks lose a wave of
+// occupancy: 77 x 4100 x 4112 takes 17 us with two, 19 to 21 with three or
+// four).  The non-temporal hint on B lost 10-30 %.
 
 template <int MT, int U, bool WHOLE>
 __device__ __forceinline__ void rows_blocks(const MatmulArgs &a, f4 (&acc)[MT], int64_t nr, const int64_t (&mr)[MT], int64_t block,
@@ -137,8 +140,8 @@ __global__ __launch_bounds__(256) void product_rows_kernel(MatmulArgs a)
         int64_t block = wave;
         if (MT == 1)
             for (; block + 28 < whole; block += 32) rows_blocks<MT, 8, true>(a, acc, nr, mr, block, part);
-        for (; block + 12 < whole; block += 16) rows_blocks<MT, 4, true>(a, acc, nr, mr, block, part);
-        for (; block < blocks; block += 4) rows_blocks<MT, 1, false>(a, acc, nr, mr, block, part);
+        for (; block + 4 < whole; block += 8) rows_blocks<MT, 2, true>(a, acc, nr, mr, block, part);
+        for (; block < blocks; block += 8) rows_blocks<MT, 2, false>(a, acc, nr, mr, block, part);
         __syncthreads();
         if (wave > 0)
 #pragma unroll
