@@ -15,8 +15,6 @@
 //  - a few rows are bound by the read of B, not by the matrix cores, and take
 //    the exact form whatever the result.
 //
-// B's rows go in as the instruction's first operand: a lane then ends with
-// neighbouring columns of C, which it stores together.
 #include "opt_pass.h"
 
 namespace optstep {
@@ -88,6 +86,9 @@ __device__ __forceinline__ void store_c(const MatmulArgs &a, int64_t m, int64_t 
     }
 }
 
+// B's rows go in as the instruction's first operand: a lane then ends with four
+// neighbouring columns of C.
+//
 // A workgroup of four waves forms 16 x MT rows of A by 16 of B; each wave sums
 // every fourth block of 128 columns and the four sums meet in LDS.  It is bound
 // by the read of B, at 3 to 4 TB/s: a wave has the pieces of two blocks in
@@ -283,9 +284,9 @@ struct LaneRow {
     }
 };
 
-__device__ __forceinline__ f16v mfma_codes(const i8v &b, int sb, const i8v &a, int sa, const f16v &c)
+__device__ __forceinline__ f16v mfma_codes(const i8v &a, int sa, const i8v &b, int sb, const f16v &c)
 {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 0, 0, 0, sb, 0, sa);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, sa, 0, sb);
 }
 
 #define SCHED() __builtin_amdgcn_sched_barrier(0)
@@ -314,7 +315,7 @@ struct Half<false, TM, TN, PF> {
             SCHED();
             before(i);
 #pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] = mfma_codes(fb[j], (int)(sb >> (8 * j)), fa[i % PF], (int)(sa >> (8 * i)), acc[i][j]);
+            for (int j = 0; j < TN; ++j) acc[i][j] = mfma_codes(fa[i % PF], (int)(sa >> (8 * i)), fb[j], (int)(sb >> (8 * j)), acc[i][j]);
             fa[i % PF] = next(i);
         }
         SCHED();
@@ -356,13 +357,53 @@ struct Half<true, TM, TN, PF> {
                 const bf8v n = widen8((uint32_t)fa[i1 % PF][2 * s1], (uint32_t)fa[i1 % PF][2 * s1 + 1], scale_of(byte));
                 if (s == 2) fa[i % PF] = next(i);
 #pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j][s], w, acc[i][j], 0, 0, 0);
+                for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, b[j][s], acc[i][j], 0, 0, 0);
                 w = n;
                 if (i == TM - 1 && s > 0) widen_b(fbn, sbn, s - 1);
             }
         }
         widen_b(fbn, sbn, 3);
         SCHED();
+    }
+};
+
+// Two neighbouring columns of C, `cnt` of which exist.
+template <int DT>
+struct Pair {
+    typedef typename Elem<DT>::T T;
+    typedef uint32_t u1_any __attribute__((aligned(2)));
+    uint32_t w[2];
+
+    __device__ __forceinline__ void load(const void *p, int64_t j, int cnt)
+    {
+        const T *q = (const T *)p + j;
+        w[0] = w[1] = 0;
+        if (cnt == 2) {
+            if (DT == kP32) {
+                const u2 v = gld<u2_any>(q);
+                w[0] = v[0];
+                w[1] = v[1];
+            } else {
+                const uint32_t v = gld<u1_any>(q);
+                w[0] = v & 0xFFFFu;
+                w[1] = v >> 16;
+            }
+        } else if (cnt == 1) {
+            w[0] = DT == kP32 ? gld<uint32_t>(q) : gld<uint16_t>(q);
+        }
+    }
+    __device__ __forceinline__ float at(int i) const { return DT == kP32 ? bitsf(w[i]) : DT == kPBF16 ? bf16_lo(w[i]) : f16_lo(w[i]); }
+
+    static __device__ __forceinline__ void store(void *p, int64_t j, int cnt, float x, float y)
+    {
+        T *q = (T *)p + j;
+        if (cnt == 2) {
+            if (DT == kP32) gst<u2_any>(q, (u2){fbits(x), fbits(y)});
+            else gst<u1_any>(q, pack2<DT>(x, y));
+        } else if (cnt == 1) {
+            if (DT == kP32) gst<float>(q, x);
+            else gst<uint16_t>(q, (uint16_t)pack2<DT>(x, 0.0f));
+        }
     }
 };
 
@@ -391,6 +432,7 @@ template <int DT, bool EXACT, int WM, int WN, int TM, int TN, int PF>
 __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(MatmulArgs a)
 {
 #if defined(__HIP_DEVICE_COMPILE__)   // the host pass has no buffer and matrix builtins, and needs the name alone
+    static_assert(TN == 2, "a lane stores two columns");
     constexpr int kThr = 64 * WM * WN, BM = 32 * TM * WM, BN = 32 * TN * WN;
     __shared__ __attribute__((aligned(16))) uint8_t la0[BM * kStage], la1[BM * kStage], lb0[BN * kStage], lb1[BN * kStage];
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), r = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
@@ -490,33 +532,29 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(MatmulArgs a
         }
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);     // vmcnt(0): no copy is on its way when the workgroup gives its LDS up
-    // lane (r, h) holds rows TM r + i of C and, of the columns TN x + j, those
-    // with x = 8 g + 4 h + e: 4 TN neighbouring ones for each g
+    // Lane (r, h) holds columns TN r + j of C and, of its rows TM x + i, those
+    // with x = 8 g + 4 h + e: a wave's store is 32 neighbouring pairs of
+    // columns in two rows.
+    const int cnt = rb < a.n ? (int)min((int64_t)TN, a.n - rb) : 0;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int64_t m = ra + i;
-        if (m >= a.m) break;
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            const int64_t n = n0 + wn + TN * (8 * g + 4 * h);
-            float v[4 * TN];
+            const int64_t m = m0 + wm + TM * (8 * g + 4 * h) + i;
+            Pair<DT> old[4];
+            if (a.accumulate)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+                for (int e = 0; e < 4; ++e) old[e].load(a.c, (m + TM * e) * a.ldc + rb, m + TM * e < a.m ? cnt : 0);
 #pragma unroll
-                for (int j = 0; j < TN; ++j) v[TN * e + j] = acc[i][j][4 * g + e];
-#pragma unroll
-            for (int p = 0; p < TN / 2; ++p) {
-                const int cnt = left8(n + 8 * p, a.n);
+            for (int e = 0; e < 4; ++e) {
+                float x = acc[i][0][4 * g + e], y = acc[i][1][4 * g + e];
                 if (a.accumulate) {
-                    float old[8];
-                    load8<DT>(a.c, m * a.ldc + n + 8 * p, cnt, old);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[8 * p + e] = old[e] + v[8 * p + e];
+                    x = old[e].at(0) + x;
+                    y = old[e].at(1) + y;
                 }
-                store8<DT>(a.c, m * a.ldc + n + 8 * p, cnt, v + 8 * p);
+                Pair<DT>::store(a.c, (m + TM * e) * a.ldc + rb, m + TM * e < a.m ? cnt : 0, x, y);
             }
         }
-    }
 #endif
 }
 
@@ -547,10 +585,11 @@ static hipError_t launch_tile(const MatmulArgs &a, hipStream_t st)
 // 64 rows 16.1 us against 16.3, 128 rows 26.4 against 16.4.  Equal at
 // ceil(m / 32) * n = 13000 (24000).
 //
-// 256 x 256 tiles read A and B half as often and run at twice the rate once
-// each compute unit has one; a round of them costs 45 us where 512 tiles of
-// 128 x 128, two a compute unit, cost 33 and up to 256 of them 28: 2048 rows
-// 46 us against 36, 11008 columns by 1024 rows 48 against 58.
+// 256 x 256 tiles read A and B half as often and run at up to 1.2 times the
+// rate, but one fills a compute unit where two of 128 x 128 fit: a round of 256
+// of them costs 45 where one of 512 small ones costs 28.  2048 rows by 4096
+// columns 46 us against 36, 2880 by 7904 99.6 against 96.8 (to fp32 178 against
+// 169), 8192 by 4096 110 against 132, 1024 by 11008 48 against 58.
 template <int DT>
 static hipError_t launch_matmul_t(const MatmulArgs &a, hipStream_t st)
 {
@@ -558,7 +597,7 @@ static hipError_t launch_matmul_t(const MatmulArgs &a, hipStream_t st)
     const bool fits = a.a.ld < kTileMaxLd && a.b.ld < kTileMaxLd && small < (1 << 22) && a.m >= 4 && a.n >= 4 && a.k >= kStage;
     if (!fits || ((a.m + 31) / 32) * a.n <= (DT == kP32 ? 24000 : 13000))
         return a.m <= 16 ? launch_rows<DT, 1>(a, st) : launch_rows<DT, 2>(a, st);
-    const int64_t tall = (large + 255) / 256 * 45, low = small <= 256 ? 28 : (small + 511) / 512 * 33;
+    const int64_t tall = (large + 255) / 256 * 45, low = (small + 511) / 512 * 28;
     return tall <= low ? launch_tile<DT, 2, 4, 4, 2, 2>(a, st) : launch_tile<DT, 2, 2, 2, 2, 1>(a, st);
 }
 
