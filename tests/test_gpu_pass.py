@@ -494,6 +494,23 @@ def test_product_slices_and_strides():
     assert np.array_equal(host(c), (av[8:48, 128:512] @ bv[4:54, 128:512].T).astype(np.float32)) and untouched(c)
 
 
+@pytest.mark.parametrize("m", [3, 300])
+def test_product_offsets_past_32_bits(m):
+    """Rows of B, and of C, whose offsets pass 2^32 bytes, in the rows kernel
+    and the tiles."""
+    import torch
+    import optimizer_step_amd as osa
+    n, k = 4400, 272
+    a, av = coded(1, m, k, True)
+    b, bv = coded(2, n, k, True)
+    big = torch.empty(n * (1 << 20), dtype=torch.uint8, device="cuda").view(n, 1 << 20)[:, 512:512 + k]
+    big.copy_(b[0])
+    ldc = (1 << 23) if m > 128 else (1 << 30)
+    c = torch.empty(m * ldc, dtype=torch.bfloat16, device="cuda").view(m, ldc)[:, 16:16 + n]
+    osa.opt_block_matmul(a, (big, b[1]), c)
+    assert np.array_equal(host(c), P.rounded(av @ bv.T, "bf16"))
+
+
 def test_product_no_columns():
     import torch
     import optimizer_step_amd as osa
