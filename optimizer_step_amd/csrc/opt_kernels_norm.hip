@@ -180,13 +180,15 @@ __device__ __forceinline__ void load_row(const NormGradArgs &a, int64_t row, Gra
 }
 
 // A workgroup takes every gridDim.x-th row (or group of rows) and keeps its
-// columns' sums of dy * (h * r) in registers; where two rows fit there, the
-// next one is on its way while this one's sums are formed.
+// columns' sums of dy * (h * r) in registers; where two rows fit there (not in
+// the 128 registers of 1024 lanes), the next one is on its way while this one's
+// sums are formed.  Rows above 16384 columns spill: 1.3 to 1.4 TB/s at 1024 x
+// 32768, against 3.9 to 4.5 at 2048 x 16384.
 template <int DT, int LANES, int VECS, bool EIGHTS>
 __global__ __launch_bounds__(norm_threads(LANES)) void rms_norm_grad_kernel(NormGradArgs a)
 {
     constexpr int kRows = norm_threads(LANES) / LANES;
-    constexpr bool kAhead = VECS * (int)sizeof(typename Elem<DT>::T) <= 8;
+    constexpr bool kAhead = LANES < 1024 && VECS * (int)sizeof(typename Elem<DT>::T) <= 8;
     __shared__ double slot[2][16][2];
     __shared__ float comb[LANES < 256 ? 256 * 8 : 1];
     const int lane = threadIdx.x % LANES;
