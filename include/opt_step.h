@@ -436,9 +436,15 @@ int opt_block_cast(const opt_cast *a, void *stream);
 
 /* c[i, j] = sum over k of a[i, k] * b[j, k], plus c[i, j] if accumulate: the
  * product of block-coded a [m, k] with the transpose of block-coded b [n, k],
- * summed in binary32 in a fixed order and rounded once on store.  k counts
- * code bytes and is a multiple of 16: a matrix whose columns are not one is
- * given with its zero padding.  A layer's three products take the layouts of
+ * summed in binary32 in a fixed order and rounded once on store.  An OPT_F32
+ * c, and any c of few rows, sums exact products (a code times its scale below
+ * 2^-126 may read as 0).  A 16-bit c of many rows takes the matrix cores'
+ * 8-bit products, which line each sixteen of them up by the largest exponent
+ * among their codes' pairs (a subnormal code counts as 2^-6) and drop what
+ * lies below 2^-13 of it: 1.5e-5 of a result on normal data, where its store
+ * rounds by 2e-4 (OPT_F16) or 2e-3 (OPT_BF16).  k counts code bytes and is a
+ * multiple of 16: a matrix whose columns are not one is given with its zero
+ * padding.  A layer's three products take the layouts of
  * opt_block_cast: y = x W^T from q(x) and q(W); dx = dy W from q(dy) and
  * qt(W); dW = dy^T x from qt(dy) and qt(x).  k = 0 gives 0 (or leaves c). */
 typedef struct {
