@@ -463,6 +463,7 @@ def opt_round_cast(x, out, stochastic=False, seed=0, offset=0, stream=None):
 # block-coded matrix is a pair (codes, scales) as block_buffers makes it.
 
 CODE_BLOCK = 128
+CODE_PRODUCTS = 2      # OPT_CODE_PRODUCTS
 
 
 def _round_up(n, m):
@@ -663,9 +664,12 @@ def opt_block_cast(x, codes=None, codes_t=None, block_rows=1, stream=None):
     return _check((_lib or lib()).opt_block_cast(ctypes.byref(a), _raw_stream(stream, dev)))
 
 
-def opt_block_matmul(a, b, out, accumulate=False, stream=None):
+def opt_block_matmul(a, b, out, accumulate=False, stream=None, exact=True):
     """out [m, n] = a b^T (+ out): a and b block-coded pairs of m and n rows
-    of the same length; out float32, bfloat16 or float16."""
+    of the same length; out float32, bfloat16 or float16.  The sum is binary32,
+    of exact products; exact=False lets a 16-bit out of many rows take the 8-bit
+    matrix products, at up to twice the rate and with the loss that the header
+    states."""
     dev = _device()
     _on_device(out, "out", dev)
     m, n, ldc = _sides(out, "out")
@@ -673,7 +677,7 @@ def opt_block_matmul(a, b, out, accumulate=False, stream=None):
     if b[0].shape[1] != k:
         raise ValueError(f"a has {k} code columns, b {b[0].shape[1]}")
     r = OptProduct(m, n, k, _coded(a, "a's", m, k, dev), _coded(b, "b's", n, k, dev), out.data_ptr(), ldc, _type(out),
-                   1 if accumulate else 0)
+                   (1 if accumulate else 0) + (0 if exact else CODE_PRODUCTS))
     return _check((_lib or lib()).opt_block_matmul(ctypes.byref(r), _raw_stream(stream, dev)))
 
 

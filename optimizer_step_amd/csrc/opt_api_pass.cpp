@@ -236,13 +236,14 @@ int opt_block_matmul(const opt_product *n, void *stream)
     if ((rc = check_dtype(n->c_dtype, "c_dtype")) != OPT_OK) return rc;
     if ((rc = check_sides(n->m, n->n)) != OPT_OK) return rc;
     if (n->k < 0 || n->k >= kMaxSide || n->k % 16 != 0) return report(OPT_EINVAL, "k must be a multiple of 16 in [0, 2^31)");
-    if (n->accumulate != 0 && n->accumulate != 1) return report(OPT_EINVAL, "accumulate must be 0 or 1");
+    if (n->accumulate & ~(1 | OPT_CODE_PRODUCTS)) return report(OPT_EINVAL, "accumulate must be 0 or 1, with or without OPT_CODE_PRODUCTS");
+    const int add = n->accumulate & 1;
     if (n->m == 0 || n->n == 0) return OPT_OK;
     if ((rc = check_matrix("c", n->c, n->ldc, n->m, n->n, size_of(n->c_dtype))) != OPT_OK) return rc;
     if (n->k > 0) {
         if ((rc = check_codes("a", n->a, n->m, n->k)) != OPT_OK) return rc;
         if ((rc = check_codes("b", n->b, n->n, n->k)) != OPT_OK) return rc;
-    } else if (n->accumulate) {
+    } else if (add) {
         return OPT_OK;
     }
     MatmulArgs a{};
@@ -253,7 +254,8 @@ int opt_block_matmul(const opt_product *n, void *stream)
     a.b = codes_of(n->b);
     a.c = n->c;
     a.ldc = n->ldc;
-    a.accumulate = n->accumulate;
+    a.accumulate = add;
+    a.exact = !(n->accumulate & OPT_CODE_PRODUCTS);
     return done(launch_block_matmul(n->c_dtype, a, (hipStream_t)stream), "block product launch");
 }
 

@@ -61,6 +61,7 @@ struct MatmulArgs {
     void *c;
     int64_t ldc;
     int accumulate;
+    int exact;             // 0: a 16-bit c may take the 8-bit products
 };
 
 // Lanes of a row and workgroups of the norm's backward pass, by the shape

@@ -132,3 +132,32 @@ def norm_gradients(dy, h, w, dh, eps):
     if dh is not None:
         size = size + np.abs(dh)
     return dx, (dy * h * r).sum(0), size, (np.abs(dy * h) * r).sum(0)
+
+
+# ---- the 8-bit matrix products ----------------------------------------------
+
+
+def exponents(codes):
+    """Floor exponents of E4M3 codes, a subnormal code's as -6, a zero's far below."""
+    c = np.asarray(codes, np.int64) & 0x7F
+    return np.where(c == 0, -1000, np.maximum(c >> 3, 1) - 7)
+
+
+def code_products_loss(qa, sa, qb, sb, k):
+    """What opt_block_matmul may lose with OPT_CODE_PRODUCTS, for rows of codes
+    qa [m, k] and qb [n, k] (k a multiple of 8) and scales [blocks, rows]: each
+    product cut toward zero at 2^-13 of 2^E, E the largest sum of exponents in
+    its eight columns.  (the sum of the losses, of their magnitudes)"""
+    m, n = qa.shape[0], qb.shape[0]
+    va, vb = e4m3(qa[:, :k]), e4m3(qb[:, :k])
+    ea, eb = exponents(qa[:, :k]), exponents(qb[:, :k])
+    loss, size = np.zeros((m, n)), np.zeros((m, n))
+    for j in range(0, k, 8):
+        e = (ea[:, None, j:j + 8] + eb[None, :, j:j + 8]).max(2, keepdims=True)
+        p = va[:, None, j:j + 8] * vb[None, :, j:j + 8]
+        unit = 2.0 ** np.maximum(e - 13.0, -60)
+        lost = p - np.trunc(p / unit) * unit
+        scale = 2.0 ** (sa[j // 128].astype(float)[:, None] + sb[j // 128].astype(float)[None, :] - 254)
+        loss += lost.sum(2) * scale
+        size += np.abs(lost).sum(2) * scale
+    return loss, size
