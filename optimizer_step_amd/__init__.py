@@ -512,7 +512,11 @@ def _type(t):
 
 
 def _raw_stream(stream, dev):
-    return _current_stream(dev) if stream is None else _stream(stream)
+    if stream is None:
+        return _current_stream(dev)
+    if getattr(stream, "device_index", dev) != dev:     # its launch would run there, on addresses of dev
+        raise ValueError(f"the stream is of device {stream.device_index}, not of the current device cuda:{dev}")
+    return _stream(stream)
 
 
 def _sides(t, what):

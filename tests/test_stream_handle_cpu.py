@@ -2,6 +2,7 @@
 short way to it."""
 import types
 
+import pytest
 import torch
 
 import optimizer_step_amd as osa
@@ -26,3 +27,10 @@ def test_current_stream_by_the_raw_handle(monkeypatch):
 def test_given_streams():
     assert osa._stream(5) == 5 and osa._raw_stream(5, 0) == 5
     assert osa._stream(types.SimpleNamespace(cuda_stream=9)) == 9
+
+
+def test_streams_of_another_device_are_refused():
+    """A launch runs on its stream's device, where the tensors' addresses may mean nothing."""
+    assert osa._raw_stream(types.SimpleNamespace(cuda_stream=9, device_index=1), 1) == 9
+    with pytest.raises(ValueError, match="device 1"):
+        osa._raw_stream(types.SimpleNamespace(cuda_stream=9, device_index=1), 0)
