@@ -311,12 +311,12 @@ int opt_round_cast(const float *x, void *out, int64_t n, int32_t out_dtype, int3
                    uint64_t offset, void *stream);
 
 /* ---- the training pass beside the step --------------------------------
- * Operators that produce the gradients the step consumes, in the numerics of
- * the rounding cast and of the FP8 states: dropout from the counter-based
- * generator, the root-mean-square norm with the residual's addition, the cast
- * to block-coded matrices, and their product.  They hold no workspace and
- * take no lock: calls may overlap on any streams, threads and devices (each
- * call runs on the current device) and be captured into graphs.
+ * Operators that produce the gradients the step consumes: dropout from the
+ * rounding cast's generator, the root-mean-square norm with the residual's
+ * addition, the cast to block-coded matrices, and their product.  They hold no
+ * workspace and take no lock: calls may overlap on any streams, threads and
+ * devices (each call runs on the current device, on a stream of that device)
+ * and be captured into graphs.
  *
  * Matrices are row-major: element (i, j) at p + i*ld + j, ld >= cols (in
  * elements; any value for one row), p aligned to its element.  Nothing
@@ -357,8 +357,9 @@ int opt_dropout(const void *x, const void *residual, void *out, int64_t n, int32
  *   r = 1/sqrt(mean(h^2) + eps), formed in binary64, rounded once to binary32;
  *   y = (h * r) * weight in binary32, rounded once on store.
  * y (in dtype) and q (block-coded, from the unrounded y, a scale for each row
- * and 128 columns) are written as given; one at least is.  A row whose mean
- * square and eps are both 0 gives NaN, as 0/0 does.  cols <= 32768. */
+ * and 128 columns) are written as given; one at least is.  r is infinite
+ * where mean(h^2) + eps is below 2^-256: zeros of such a row give NaN, as 0/0
+ * does, its other elements infinities.  cols <= 32768. */
 typedef struct {
     int64_t rows, cols;
     int32_t dtype;             /* OPT_F32, OPT_BF16 or OPT_F16: x, residual, h, y      */
@@ -438,9 +439,9 @@ int opt_block_cast(const opt_cast *a, void *stream);
  * product of block-coded a [m, k] with the transpose of block-coded b [n, k].
  * Exact products are summed in binary32 and rounded once on store (a code
  * times its scale below 2^-126 may read as 0, one of 2^128 or more as an
- * infinity: opt_block_cast writes neither for normal values).  The order of the
- * sum is fixed by m, n, k, c_dtype and OPT_CODE_PRODUCTS; a row's result may
- * differ by that order, as binary32 sums do, where m differs.
+ * infinity).  The sizes, strides, c_dtype and OPT_CODE_PRODUCTS fix the order
+ * of the sum; a row's result may differ by that order, as binary32 sums do,
+ * where m differs.
  * OPT_CODE_PRODUCTS, added to accumulate, lets an OPT_BF16 or OPT_F16 c of many
  * rows (ceil(m/32) * n > 13000, m, n >= 4, k >= 128) be summed by the matrix
  * cores' 8-bit products, at up to twice the rate.  Those cut each product
@@ -454,9 +455,9 @@ int opt_block_cast(const opt_cast *a, void *stream);
  * one is given with its zero padding.  A layer's three products take the
  * layouts of opt_block_cast: y = x W^T from q(x) and q(W); dx = dy W from q(dy)
  * and qt(W); dW = dy^T x from qt(dy) and qt(x).  k = 0 gives 0 (or leaves c).
- * Any size is right, but code rows 2^23 bytes or more apart, and results of
- * 2^22 or more 128 x 128 tiles, are formed by the kernel for few rows, which
- * reads b once for every 32 rows of a. */
+ * Products of k < 128, of code rows 2^23 bytes or more apart, and of 2^22 or
+ * more 128 x 128 tiles of c are formed by the kernel for few rows, which reads
+ * b once for every 32 rows of a: as right, and slower by up to 6 times. */
 #define OPT_CODE_PRODUCTS 2
 
 typedef struct {

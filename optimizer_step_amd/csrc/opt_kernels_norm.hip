@@ -13,7 +13,8 @@
 // words) a lane at a time, so that a 128-column block is one 16-lane DPP row
 // and its largest magnitude takes four DPP steps.  Squares are summed in
 // binary64, whose rate is half of binary32's here and leaves the kernel bound
-// by memory: r is then the same bits in whatever order the sum ran.
+// by memory: r, rounded to binary32, then hardly ever depends on the order of
+// the sum (only where a few binary64 units straddle a rounding border).
 #include "opt_pass.h"
 
 namespace optstep {
@@ -182,8 +183,10 @@ __device__ __forceinline__ void load_row(const NormGradArgs &a, int64_t row, Gra
 // A workgroup takes every gridDim.x-th row (or group of rows) and keeps its
 // columns' sums of dy * (h * r) in registers; where two rows fit there (not in
 // the 128 registers of 1024 lanes), the next one is on its way while this one's
-// sums are formed.  Rows above 16384 columns spill: 1.3 to 1.4 TB/s at 1024 x
-// 32768, against 3.9 to 4.5 at 2048 x 16384.
+// sums are formed.  1024 lanes spill: above 16384 columns 212 to 535 registers
+// (250 to 1634 where single elements are handled too), 1.5 TB/s at 1024 x 32768
+// bf16; for 8193 to 16384 columns 6 or 8 (2 to 17; fp32 362), 4.2 TB/s at
+// 2048 x 16384 and 3.0 at 2048 x 16383.
 template <int DT, int LANES, int VECS, bool EIGHTS>
 __global__ __launch_bounds__(norm_threads(LANES)) void rms_norm_grad_kernel(NormGradArgs a)
 {
