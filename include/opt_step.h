@@ -471,6 +471,179 @@ typedef struct {
 
 int opt_block_matmul(const opt_product *a, void *stream);
 
+/* The gated activation y = s(gate) * up, with s(x) = x sigma(p(x)), sigma the
+ * logistic function:  OPT_SILU p(x) = x;  OPT_GELU p(x) = 2 sqrt(2/pi) (x +
+ * 0.044715 x^3), which is 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))).
+ * Formed in binary32 and rounded once on store: y in dtype and/or q, y's
+ * codes (a scale for each row and 128 columns, as opt_block_cast makes them).
+ * gate_q and up_q receive the codes of gate and up: kept in their place until
+ * the backward pass, which takes either.  One output at least is given.  y may
+ * be gate or up.  An infinite gate gives what the formula gives: NaN at minus
+ * infinity.  gate and up are two matrices, or the halves of one [rows, 2 cols]
+ * (ldg = ldu = 2 cols). */
+#define OPT_SILU 0
+#define OPT_GELU 1
+
+typedef struct {
+    int64_t rows, cols;
+    int32_t dtype;             /* OPT_F32, OPT_BF16 or OPT_F16: gate, up, y */
+    int32_t act;               /* OPT_SILU or OPT_GELU                      */
+    const void *gate;
+    int64_t ldg;
+    const void *up;
+    int64_t ldu;
+    void *y;                   /* or NULL                                   */
+    int64_t ldy;
+    opt_codes q, gate_q, up_q; /* codes NULL for none                       */
+} opt_gate;
+
+int opt_gated_act(const opt_gate *a, void *stream);
+
+/* Its backward pass, from dy and from gate and up, as matrices or (gate and up
+ * NULL) as the codes the forward pass kept, whose values it then
+ * differentiates at:
+ *   dgate = dy * up * s'(gate),  dup = dy * s(gate),  y = s(gate) * up,
+ *   s'(x) = sigma (1 + x (1 - sigma) p'(x)).
+ * Outputs, each where it is given: dgate and dup in dtype; their codes
+ * (dgate_q, dup_q [rows, cols]) and the codes of their transposes (dgate_t,
+ * dup_t [cols, rows]); and y_t, the codes of y's transpose, which the
+ * following product's weight gradient takes.  All from the unrounded binary32
+ * values.  dgate may be dy, gate or up, dup likewise; they must differ.  Where
+ * cols is a multiple of 128, dgate_q and dup_q may be the halves of one coded
+ * matrix [rows, 2 cols] (codes + cols, scales + cols/128 * lds), and where it
+ * is a multiple of 4, dgate_t and dup_t those of one [2 cols, rows]. */
+typedef struct {
+    int64_t rows, cols;
+    int32_t dtype;             /* OPT_F32, OPT_BF16 or OPT_F16: dy, gate, up, dgate, dup */
+    int32_t act;               /* OPT_SILU or OPT_GELU                                   */
+    const void *dy;
+    int64_t lddy;
+    const void *gate;          /* with up, or both NULL and gate_q, up_q given           */
+    int64_t ldg;
+    const void *up;
+    int64_t ldu;
+    opt_codes gate_q, up_q;
+    void *dgate;               /* or NULL                                                */
+    int64_t lddg;
+    void *dup;                 /* or NULL                                                */
+    int64_t lddu;
+    opt_codes dgate_q, dup_q, dgate_t, dup_t, y_t;   /* codes NULL for none              */
+} opt_gate_grad;
+
+int opt_gated_act_backward(const opt_gate_grad *a, void *stream);
+
+/* What a block-coded matrix q [rows, cols] holds: as the matrix x (code times
+ * scale, rounded once to dtype) and/or as qt, the codes of its transpose [cols,
+ * rows] with a scale for each of its rows and 128 columns, as opt_block_cast
+ * would make them of x in binary32.  A product's own left operand, q(x), is
+ * then the checkpoint of its weight gradient.  Values below 2^-126 and above
+ * the range of dtype round as the type's do; a block of scale byte 255 reads
+ * as NaN. */
+typedef struct {
+    int64_t rows, cols;
+    opt_codes q;
+    void *x;                   /* or NULL                                      */
+    int64_t ldx;
+    int32_t dtype;             /* OPT_F32, OPT_BF16 or OPT_F16: x              */
+    int32_t reserved;          /* 0                                            */
+    opt_codes qt;              /* codes NULL for none                          */
+} opt_restore;
+
+int opt_block_restore(const opt_restore *a, void *stream);
+
+/* The norm of each head of the queries and of the keys, and the rotation by
+ * position, in one pass.  For each token and head x of dim elements:
+ *   r = 1/sqrt(mean(x^2) + eps), formed in binary64, rounded once to binary32;
+ *   n = (x * r) * weight;
+ *   the first rot elements of n turn in pairs (a, b), elements i and i + rot/2
+ *   (interleaved: 2 i and 2 i + 1), to (a c_i - b s_i, b c_i + a s_i), i < rot/2,
+ * in binary32, rounded once on store.  c_i and s_i stand in row p of the
+ * table, p the token's position: c_0 .. c_(rot/2 - 1), then s_0 ... .  A
+ * token whose position the table does not hold gets NaNs.  rot = 0: the norm
+ * alone (the table is not read).
+ * Strides count elements: element j of head h of token t is x[t*x_token +
+ * h*x_head + j].  Any non-negative input strides; outputs keep their heads
+ * apart, either all heads of a token before the next token's or the other way
+ * round.  y may be x with the same strides.  codes receives x's codes, in rows
+ * token*heads + head of dim columns, for the backward pass.  1 <= dim <= 512,
+ * heads < 65536; either set may have no heads.  Queries and keys must not
+ * overlap in what is written. */
+typedef struct {
+    const float *cos_sin;      /* [rows][ld], rot floats of each row used              */
+    int64_t rows, ld;
+    const void *positions;     /* device, tokens integers; NULL: token t stands at t   */
+    int32_t position_bits;     /* 32 or 64                                             */
+    int32_t reserved;          /* 0                                                    */
+} opt_head_table;
+
+typedef struct {
+    int64_t heads;             /* 0 for none                                           */
+    const void *x;
+    int64_t x_token, x_head;
+    const void *weight;        /* dim elements of w_dtype, or NULL for ones            */
+    void *y;
+    int64_t y_token, y_head;
+    opt_codes codes;           /* codes NULL for none                                  */
+} opt_head_set;
+
+typedef struct {
+    int64_t tokens;
+    int32_t dim, rot;          /* rot even, 0 <= rot <= dim                            */
+    int32_t dtype, w_dtype;    /* OPT_F32, OPT_BF16 or OPT_F16: x, y; weight           */
+    int32_t interleaved;       /* 0 or 1                                               */
+    int32_t reserved;          /* 0                                                    */
+    double eps;                /* >= 0                                                 */
+    opt_head_table table;
+    opt_head_set q, k;
+} opt_heads;
+
+int opt_head_norm(const opt_heads *a, void *stream);
+
+/* Its backward pass, from dy, the gradient of y, and x as the forward pass had
+ * it or (x NULL, both sets alike) its codes:
+ *   dn = dy turned the other way,  g = dn * weight,
+ *   c = mean(g * x)  (both sums of a head in binary64),
+ *   dx = r * (g - x * (r^2 c)),
+ *   dweight = sum over tokens and heads of dn * (x * r).
+ * The sums over tokens run in a fixed order (no atomics): binary32 within a
+ * workgroup's heads, binary64 across workgroups.  dx may be dy with the same
+ * strides.  A token whose position the table does not hold gets NaNs, and they
+ * reach dweight.  With no heads or tokens a dweight becomes 0 (or stays, with
+ * accumulate). */
+typedef struct {
+    int64_t heads;             /* 0 for none                                           */
+    const void *dy;
+    int64_t dy_token, dy_head;
+    const void *x;             /* or NULL, and codes                                   */
+    int64_t x_token, x_head;
+    opt_codes codes;
+    const void *weight;        /* dim elements of w_dtype, or NULL for ones            */
+    void *dx;
+    int64_t dx_token, dx_head;
+    float *dweight;            /* dim floats, or NULL for none                         */
+} opt_head_grad_set;
+
+typedef struct {
+    int64_t tokens;
+    int32_t dim, rot;
+    int32_t dtype, w_dtype;    /* OPT_F32, OPT_BF16 or OPT_F16: dy, x, dx; weight      */
+    int32_t interleaved;       /* 0 or 1                                               */
+    int32_t accumulate;        /* 1: dweight += , 0: dweight =                         */
+    double eps;
+    opt_head_table table;
+    opt_head_grad_set q, k;
+    void *workspace;           /* device scratch of opt_head_norm_workspace bytes,
+                                  16-byte aligned, free again when the call's work has
+                                  run; NULL without dweight                            */
+    int64_t workspace_bytes;
+} opt_heads_grad;
+
+int opt_head_norm_backward(const opt_heads_grad *a, void *stream);
+
+/* Bytes of workspace opt_head_norm_backward needs for dweight at these sizes,
+ * or a negative status.  Host only. */
+int64_t opt_head_norm_workspace(int64_t tokens, int64_t heads_q, int64_t heads_k, int32_t dim);
+
 /* Test hook: the FP8/FP4 element codec of the state formats.  elem 0 = E4M3,
  * 1 = E2M1, 2 = unsigned E2M2.  For i < n: codes[i] = the code of x[i] in a
  * block whose absmax is A (A >= 0 or NaN), nearest-even if r is NULL, else

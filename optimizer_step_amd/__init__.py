@@ -93,6 +93,56 @@ class OptProduct(ctypes.Structure):
                 ("c", ctypes.c_void_p), ("ldc", ctypes.c_int64), ("c_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
 
 
+class OptGate(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("up", ctypes.c_void_p), ("ldu", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("q", OptCodes), ("gate_q", OptCodes), ("up_q", OptCodes)]
+
+
+class OptGateGrad(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64),
+                ("up", ctypes.c_void_p), ("ldu", ctypes.c_int64), ("gate_q", OptCodes), ("up_q", OptCodes),
+                ("dgate", ctypes.c_void_p), ("lddg", ctypes.c_int64), ("dup", ctypes.c_void_p), ("lddu", ctypes.c_int64),
+                ("dgate_q", OptCodes), ("dup_q", OptCodes), ("dgate_t", OptCodes), ("dup_t", OptCodes), ("y_t", OptCodes)]
+
+
+class OptRestore(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("q", OptCodes), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32), ("qt", OptCodes)]
+
+
+class OptHeadTable(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("rows", ctypes.c_int64), ("ld", ctypes.c_int64), ("positions", ctypes.c_void_p),
+                ("position_bits", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class OptHeadSet(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int64), ("x", ctypes.c_void_p), ("x_token", ctypes.c_int64), ("x_head", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("y", ctypes.c_void_p), ("y_token", ctypes.c_int64), ("y_head", ctypes.c_int64),
+                ("codes", OptCodes)]
+
+
+class OptHeads(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("dim", ctypes.c_int32), ("rot", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("w_dtype", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("reserved", ctypes.c_int32), ("eps", ctypes.c_double),
+                ("table", OptHeadTable), ("q", OptHeadSet), ("k", OptHeadSet)]
+
+
+class OptHeadGradSet(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int64), ("dy", ctypes.c_void_p), ("dy_token", ctypes.c_int64), ("dy_head", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("x_token", ctypes.c_int64), ("x_head", ctypes.c_int64), ("codes", OptCodes),
+                ("weight", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("dx_token", ctypes.c_int64), ("dx_head", ctypes.c_int64),
+                ("dweight", ctypes.c_void_p)]
+
+
+class OptHeadsGrad(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("dim", ctypes.c_int32), ("rot", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("w_dtype", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("accumulate", ctypes.c_int32), ("eps", ctypes.c_double),
+                ("table", OptHeadTable), ("q", OptHeadGradSet), ("k", OptHeadGradSet),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -136,6 +186,12 @@ def lib():
             "opt_rms_norm_backward": ([ctypes.POINTER(OptNormGrad), vp], i32),
             "opt_block_cast": ([ctypes.POINTER(OptCast), vp], i32),
             "opt_block_matmul": ([ctypes.POINTER(OptProduct), vp], i32),
+            "opt_gated_act": ([ctypes.POINTER(OptGate), vp], i32),
+            "opt_gated_act_backward": ([ctypes.POINTER(OptGateGrad), vp], i32),
+            "opt_block_restore": ([ctypes.POINTER(OptRestore), vp], i32),
+            "opt_head_norm": ([ctypes.POINTER(OptHeads), vp], i32),
+            "opt_head_norm_workspace": ([i64, i64, i64, i32], i64),
+            "opt_head_norm_backward": ([ctypes.POINTER(OptHeadsGrad), vp], i32),
             "opt_debug_mini_host": ([i32, ctypes.c_float, vp, vp, vp, vp, i64], i32),
         }
         for name, (args, res) in sig.items():
@@ -688,6 +744,238 @@ def opt_block_matmul(a, b, out, accumulate=False, stream=None, exact=True):
     r = OptProduct(m, n, k, _coded(a, "a's", m, k, dev), _coded(b, "b's", n, k, dev), out.data_ptr(), ldc, _type(out),
                    (1 if accumulate else 0) + (0 if exact else CODE_PRODUCTS))
     return _check((_lib or lib()).opt_block_matmul(ctypes.byref(r), _raw_stream(stream, dev)))
+
+
+SILU, GELU = 0, 1
+ACTIVATIONS = {"silu": SILU, "gelu": GELU}
+
+
+def _act(act):
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+    return code
+
+
+def opt_gated_act(gate, up, act="silu", y=None, codes=None, gate_codes=None, up_codes=None, stream=None):
+    """y = s(gate) * up, s the activation "silu" or "gelu" (its tanh form):
+    into y (of gate's type) and/or codes (a block-coded pair).  gate_codes and
+    up_codes receive the codes of gate and up, which opt_gated_act_backward
+    takes in their place.  gate and up are two matrices, or the halves of one:
+    z[:, :n], z[:, n:]."""
+    dev = _device()
+    _on_device(gate, "gate", dev)
+    rows, cols, ldg = _sides(gate, "gate")
+    if up is None:
+        raise ValueError("up must be a CUDA tensor")
+    pu, ldu = _like(up, "up", gate, rows, cols, dev)
+    py, ldy = _like(y, "y", gate, rows, cols, dev)
+    a = OptGate(rows, cols, _type(gate), _act(act), gate.data_ptr(), ldg, pu, ldu, py, ldy, _coded(codes, "codes'", rows, cols, dev),
+                _coded(gate_codes, "gate_codes'", rows, cols, dev), _coded(up_codes, "up_codes'", rows, cols, dev))
+    return _check((_lib or lib()).opt_gated_act(ctypes.byref(a), _raw_stream(stream, dev)))
+
+
+def opt_gated_act_backward(dy, gate, up, act="silu", dgate=None, dup=None, dgate_codes=None, dup_codes=None, dgate_codes_t=None,
+                           dup_codes_t=None, y_codes_t=None, stream=None):
+    """Gradients of opt_gated_act from dy and from gate and up: the matrices,
+    or the pairs of codes the forward pass kept.  Each output where it is
+    given: dgate and dup (of dy's type), their codes, the codes of their
+    transposes, and those of y's transpose for the next product's weight
+    gradient."""
+    dev = _device()
+    _on_device(dy, "dy", dev)
+    rows, cols, lddy = _sides(dy, "dy")
+    pg = pu = None
+    ldg = ldu = 0
+    gq = uq = OptCodes()
+    if isinstance(gate, (tuple, list)) and isinstance(up, (tuple, list)):
+        gq, uq = _coded(gate, "gate's", rows, cols, dev), _coded(up, "up's", rows, cols, dev)
+    elif hasattr(gate, "data_ptr") and hasattr(up, "data_ptr"):
+        pg, ldg = _like(gate, "gate", dy, rows, cols, dev)
+        pu, ldu = _like(up, "up", dy, rows, cols, dev)
+    else:
+        raise ValueError("gate and up must be two CUDA tensors or two pairs of codes and scales")
+    px, lddg = _like(dgate, "dgate", dy, rows, cols, dev)
+    pz, lddu = _like(dup, "dup", dy, rows, cols, dev)
+    a = OptGateGrad(rows, cols, _type(dy), _act(act), dy.data_ptr(), lddy, pg, ldg, pu, ldu, gq, uq, px, lddg, pz, lddu,
+                    _coded(dgate_codes, "dgate_codes'", rows, cols, dev), _coded(dup_codes, "dup_codes'", rows, cols, dev),
+                    _coded(dgate_codes_t, "dgate_codes_t's", cols, rows, dev), _coded(dup_codes_t, "dup_codes_t's", cols, rows, dev),
+                    _coded(y_codes_t, "y_codes_t's", cols, rows, dev))
+    return _check((_lib or lib()).opt_gated_act_backward(ctypes.byref(a), _raw_stream(stream, dev)))
+
+
+def opt_block_restore(codes, out=None, codes_t=None, stream=None):
+    """What a block-coded pair holds: as a matrix (out, float32, bfloat16 or
+    float16) and/or as the codes of its transpose (codes_t, a pair for cols x
+    rows)."""
+    dev = _device()
+    rows = codes[0].shape[0]
+    px, ldx, kind = None, 0, OPT_F32
+    if out is not None:
+        _on_device(out, "out", dev)
+        r, cols, ldx = _sides(out, "out")
+        if r != rows:
+            raise ValueError(f"out has {r} rows, codes {rows}")
+        px, kind = out.data_ptr(), _type(out)
+    elif codes_t is not None:
+        cols = codes_t[0].shape[0]
+    else:
+        raise ValueError("neither out nor codes_t is given")
+    a = OptRestore(rows, cols, _coded(codes, "codes'", rows, cols, dev), px, ldx, kind, 0, _coded(codes_t, "codes_t's", cols, rows, dev))
+    return _check((_lib or lib()).opt_block_restore(ctypes.byref(a), _raw_stream(stream, dev)))
+
+
+def rotation_table(positions, rot, base=10000.0, device="cuda"):
+    """cos and sin of the angles p * base^(-2 i / rot), i < rot/2, for the
+    positions p < positions: float32 [positions, rot], the cosines first, each
+    formed in binary64 and rounded once."""
+    import torch
+    f = base ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+    a = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * f
+    return torch.cat([a.cos(), a.sin()], 1).float()
+
+
+def _head_rows(t, what, like, shape, dev):
+    """(pointer, stride of a token, stride of a head) of heads [tokens, heads,
+    dim] whose elements are neighbours."""
+    if t is None:
+        raise ValueError(f"{what} is missing")
+    if t.get_device() != dev:
+        _on_device(t, what, dev)
+    if t.dtype != like:
+        raise ValueError(f"{what} is {t.dtype}, not {like}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+    st = t.stride()
+    if st[2] != 1 and shape[2] > 1:
+        raise ValueError(f"{what} must have contiguous heads")
+    return t.data_ptr(), st[0], st[1]
+
+
+def _head_table(table, positions, tokens, dev):
+    """(the record, rot) of a rotation's table and positions."""
+    if table is None:
+        return OptHeadTable(None, 0, 0, None, 64, 0), 0
+    import torch
+    _on_device(table, "table", dev)
+    if table.dtype != torch.float32 or table.dim() != 2 or (table.stride(1) != 1 and table.shape[1] > 1):
+        raise ValueError("table must be float32 [positions, rot] with contiguous rows")
+    rows, rot = table.shape
+    ld = table.stride(0) if rows > 1 else rot
+    if positions is None:
+        return OptHeadTable(table.data_ptr(), rows, ld, None, 64, 0), rot
+    _on_device(positions, "positions", dev)
+    bits = 64 if positions.dtype == torch.int64 else 32
+    if (bits == 32 and positions.dtype != torch.int32) or positions.numel() != tokens or not positions.is_contiguous():
+        raise ValueError(f"positions must be {tokens} contiguous int64 or int32")
+    return OptHeadTable(table.data_ptr(), rows, ld, positions.data_ptr(), bits, 0), rot
+
+
+def _head_weights(weight_q, weight_k, dim, dev):
+    """(pointer, pointer, type) of the two sets' weights, either None."""
+    pq = pk = None
+    dt = OPT_F32
+    if weight_q is not None:
+        pq, dt = _weight(weight_q, dim, dev)
+    if weight_k is not None:
+        pk, dk = _weight(weight_k, dim, dev)
+        if pq is not None and dk != dt:
+            raise ValueError("weight_q and weight_k must be of one type")
+        dt = dk
+    return pq, pk, dt
+
+
+def opt_head_norm(q, k, weight_q=None, weight_k=None, table=None, positions=None, eps=1e-6, interleaved=False, q_out=None, k_out=None,
+                  q_codes=None, k_codes=None, stream=None):
+    """The RMS norm of each head of q [tokens, heads, dim] and k [tokens, kv
+    heads, dim] (None: queries alone) times its weight (dim elements; None:
+    ones), then the rotation of the first table.shape[1] elements by the angles
+    that row positions[t] of table holds (rotation_table makes one; None: no
+    rotation; positions None: token t stands at row t), in pairs half of them
+    apart, or next to each other (interleaved).  Into q_out and k_out: of the
+    shape and type of q and k, which may be views, such as parts of one
+    product's result or transposed [heads, tokens, dim].  q_codes and k_codes
+    (block-coded pairs for tokens * heads x dim) receive the codes of q and k,
+    which the backward pass takes in their place."""
+    dev = _device()
+    _on_device(q, "q", dev)
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, dim]")
+    shape, dtype = q.shape, q.dtype
+    tokens, heads, dim = shape
+    tab, rot = _head_table(table, positions, tokens, dev)
+    pwq, pwk, wd = _head_weights(weight_q, weight_k, dim, dev)
+    sq = OptHeadSet(heads, *_head_rows(q, "q", dtype, shape, dev), pwq, *_head_rows(q_out, "q_out", dtype, shape, dev),
+                    _coded(q_codes, "q_codes'", tokens * heads, dim, dev))
+    sk = OptHeadSet()
+    if k is not None:
+        if k.dim() != 3 or k.shape[0] != tokens or k.shape[2] != dim:
+            raise ValueError(f"k must be [{tokens}, heads, {dim}], got {list(k.shape)}")
+        shape = k.shape
+        sk = OptHeadSet(shape[1], *_head_rows(k, "k", dtype, shape, dev), pwk, *_head_rows(k_out, "k_out", dtype, shape, dev),
+                        _coded(k_codes, "k_codes'", tokens * shape[1], dim, dev))
+    a = OptHeads(tokens, dim, rot, _type(q), wd, 1 if interleaved else 0, 0, float(eps), tab, sq, sk)
+    return _check((_lib or lib()).opt_head_norm(ctypes.byref(a), _raw_stream(stream, dev)))
+
+
+def opt_head_norm_workspace(tokens, heads_q, heads_k, dim):
+    """Bytes of device workspace opt_head_norm_backward takes for its weights'
+    gradients."""
+    n = lib().opt_head_norm_workspace(int(tokens), int(heads_q), int(heads_k), int(dim))
+    if n < 0:
+        _check(int(n))
+    return int(n)
+
+
+def opt_head_norm_backward(dq_out, dk_out, q, k, weight_q=None, weight_k=None, table=None, positions=None, eps=1e-6, interleaved=False,
+                           dq=None, dk=None, dweight_q=None, dweight_k=None, accumulate=False, workspace=None, stream=None):
+    """Gradients of opt_head_norm: dq and dk, and dweight_q and dweight_k
+    (float32; added to with accumulate; None: not formed) from the gradients
+    dq_out and dk_out (None: queries alone) of its results and from q and k as
+    it had them, or the pairs of codes it kept.  workspace: a CUDA byte tensor
+    of opt_head_norm_workspace(...), or None to take one from torch's
+    allocator."""
+    import torch
+    dev = _device()
+    _on_device(dq_out, "dq_out", dev)
+    if dq_out.dim() != 3:
+        raise ValueError("dq_out must be [tokens, heads, dim]")
+    dtype = dq_out.dtype
+    tokens, heads, dim = dq_out.shape
+    tab, rot = _head_table(table, positions, tokens, dev)
+    pwq, pwk, wd = _head_weights(weight_q, weight_k, dim, dev)
+
+    def one(dy, x, w, dx, dw, name):
+        shape = dy.shape
+        if dy.dim() != 3 or shape[0] != tokens or shape[2] != dim:
+            raise ValueError(f"d{name}_out must be [{tokens}, heads, {dim}], got {list(shape)}")
+        if isinstance(x, (tuple, list)):
+            rows = (None, 0, 0, _coded(x, f"{name}'s", tokens * shape[1], dim, dev))
+        else:
+            rows = (*_head_rows(x, name, dtype, shape, dev), OptCodes())
+        if dw is not None:
+            _device_buffer(dw, 4, dim, f"dweight_{name}")
+            if dw.dtype != torch.float32:
+                raise ValueError(f"dweight_{name} must be a CUDA float32 tensor")
+        return OptHeadGradSet(shape[1], *_head_rows(dy, f"d{name}_out", dtype, shape, dev), *rows, w,
+                              *_head_rows(dx, f"d{name}", dtype, shape, dev), _ptr(dw))
+
+    sq = one(dq_out, q, pwq, dq, dweight_q, "q")
+    sk = OptHeadGradSet()
+    if dk_out is None and (dk is not None or dweight_k is not None):
+        raise ValueError("dk and dweight_k need dk_out")
+    if dk_out is not None:
+        sk = one(dk_out, k, pwk, dk, dweight_k, "k")
+    need = 0
+    if dweight_q is not None or dweight_k is not None:
+        need = opt_head_norm_workspace(tokens, heads, sk.heads, dim)
+        if workspace is None:
+            workspace = _scratch(need, stream)
+        else:
+            _device_buffer(workspace, 1, need, "workspace")
+    a = OptHeadsGrad(tokens, dim, rot, _type(dq_out), wd, 1 if interleaved else 0, 1 if accumulate else 0, float(eps), tab, sq, sk,
+                     _ptr(workspace) if need else None, need)
+    return _check((_lib or lib()).opt_head_norm_backward(ctypes.byref(a), _raw_stream(stream, dev)))
 
 
 def opt_debug_mini(elem, A, x, r, codes, decoded, stream=None):

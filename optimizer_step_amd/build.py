@@ -19,7 +19,8 @@ SOURCES = [("opt_api.cpp", []), ("opt_kernels.hip", []), ("opt_kernels_ew.hip", 
            ("opt_kernels_q8.hip", ["-DOPT_Q8_PD=0"]), ("opt_kernels_q8.hip", ["-DOPT_Q8_PD=1"]),
            ("opt_kernels_q8.hip", ["-DOPT_Q8_PD=2"]),
            ("opt_api_pass.cpp", []), ("opt_kernels_drop.hip", []), ("opt_kernels_norm.hip", []),
-           ("opt_kernels_cast.hip", []), ("opt_kernels_mm.hip", [])]
+           ("opt_kernels_cast.hip", []), ("opt_kernels_mm.hip", []),
+           ("opt_kernels_gate.hip", []), ("opt_kernels_heads.hip", [])]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

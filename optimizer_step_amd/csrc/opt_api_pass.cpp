@@ -18,6 +18,11 @@ hipError_t launch_rms_norm(int dt, const NormArgs &a, hipStream_t st);
 hipError_t launch_rms_norm_grad(int dt, const NormGradArgs &a, float *dw, int accumulate, hipStream_t st);
 hipError_t launch_block_cast(int dt, const CastArgs &a, int square, hipStream_t st);
 hipError_t launch_block_matmul(int dt, const MatmulArgs &a, hipStream_t st);
+hipError_t launch_gated_act(int dt, int act, const GateArgs &a, hipStream_t st);
+hipError_t launch_gated_act_grad(int dt, int act, const GateGradArgs &a, hipStream_t st);
+hipError_t launch_block_restore(int dt, const RestoreArgs &a, hipStream_t st);
+hipError_t launch_head_norm(int dt, const HeadArgs &a, hipStream_t st);
+hipError_t launch_head_norm_grad(int dt, int coded, const HeadGradArgs &a, float *dwq, float *dwk, int accumulate, hipStream_t st);
 
 namespace {
 
@@ -74,6 +79,90 @@ int check_codes(const char *what, const opt_codes &q, int64_t rows, int64_t byte
 }
 
 Codes codes_of(const opt_codes &q) { return Codes{q.codes, q.ld, q.scales, q.lds}; }
+
+// An optional output.
+int check_more(const char *what, const void *p, int64_t ld, int64_t rows, int64_t cols, size_t size)
+{
+    return p ? check_matrix(what, p, ld, rows, cols, size) : OPT_OK;
+}
+
+int check_more(const char *what, const opt_codes &q, int64_t rows, int64_t bytes)
+{
+    return q.codes ? check_codes(what, q, rows, bytes) : OPT_OK;
+}
+
+int check_act(int32_t act)
+{
+    return act == OPT_SILU || act == OPT_GELU ? OPT_OK : report(OPT_EINVAL, "unknown activation %d", act);
+}
+
+// Heads of dim elements, `token` and `head` elements apart.  Outputs lie apart
+// from each other: heads within a token, or tokens within a head.
+int check_heads(const char *what, const void *p, int64_t token, int64_t head, int64_t tokens, int64_t heads, int64_t dim, size_t size, bool out)
+{
+    if (!p) return report(OPT_EINVAL, "%s is NULL", what);
+    if (!at(p, size)) return report(OPT_EALIGN, "%s must be aligned to its %d-byte elements", what, (int)size);
+    if ((tokens > 1 && token < 0) || (heads > 1 && head < 0)) return report(OPT_EINVAL, "%s: negative stride", what);
+    if ((tokens > 1 && token > kMaxElems / tokens) || (heads > 1 && head > kMaxElems / heads))
+        return report(OPT_EINVAL, "%s: tokens or heads times their stride above 2^46", what);
+    if (out) {
+        const bool inner = heads == 1 || head >= dim, outer = tokens == 1 || token >= dim;
+        const bool by_token = tokens == 1 || token >= (heads - 1) * head + dim, by_head = heads == 1 || head >= (tokens - 1) * token + dim;
+        if (!inner || !outer || !(by_token || by_head)) return report(OPT_EINVAL, "%s: its heads overlap", what);
+    }
+    return OPT_OK;
+}
+
+int check_turn(int64_t tokens, int32_t dim, int32_t rot, int32_t dtype, int32_t w_dtype, int32_t interleaved, double eps)
+{
+    int rc;
+    if ((rc = check_dtype(dtype, "dtype")) != OPT_OK) return rc;
+    if ((rc = check_dtype(w_dtype, "w_dtype")) != OPT_OK) return rc;
+    if (tokens < 0 || tokens >= kMaxSide) return report(OPT_EINVAL, "tokens must lie in [0, 2^31)");
+    if (dim < 1) return report(OPT_EINVAL, "dim must be positive");
+    if (dim > kMaxHeadDim) return report(OPT_EUNSUPPORTED, "heads above %d elements", kMaxHeadDim);
+    if (rot < 0 || rot > dim || rot % 2 != 0) return report(OPT_EINVAL, "rot must be even, in [0, dim]");
+    if (interleaved != 0 && interleaved != 1) return report(OPT_EINVAL, "interleaved must be 0 or 1");
+    if (!(eps >= 0.0) || std::isinf(eps)) return report(OPT_EINVAL, "eps must be a non-negative number");
+    return OPT_OK;
+}
+
+int check_table(const opt_head_table &t, int64_t tokens, int32_t rot)
+{
+    if (rot == 0 || tokens == 0) return OPT_OK;
+    if (t.position_bits != 32 && t.position_bits != 64) return report(OPT_EINVAL, "position_bits must be 32 or 64");
+    if (t.rows < 1 || t.rows >= kMaxSide) return report(OPT_EINVAL, "the table's rows must lie in [1, 2^31)");
+    int rc;
+    if ((rc = check_matrix("table", t.cos_sin, t.ld, t.rows, rot, 4)) != OPT_OK) return rc;
+    if (!t.positions && tokens > t.rows) return report(OPT_EINVAL, "the table holds %lld positions of %lld", (long long)t.rows, (long long)tokens);
+    if (!at(t.positions, (size_t)t.position_bits / 8)) return report(OPT_EALIGN, "positions must be aligned to their elements");
+    return OPT_OK;
+}
+
+int check_count(const char *what, int64_t heads, int64_t tokens, bool coded)
+{
+    if (heads < 0 || heads >= 65536) return report(OPT_EINVAL, "%s: heads must lie in [0, 65536)", what);
+    if (coded && heads * tokens >= kMaxSide) return report(OPT_EINVAL, "%s: coded tokens times heads must be below 2^31", what);
+    return OPT_OK;
+}
+
+HeadTurn turn_of(int64_t tokens, int32_t dim, int32_t rot, int32_t w_dtype, int32_t interleaved, double eps, const opt_head_table &t)
+{
+    HeadTurn r{};
+    r.tokens = tokens;
+    r.table_rows = t.rows;
+    r.ldt = t.ld;
+    r.table = t.cos_sin;
+    r.positions = t.positions;
+    r.dim = dim;
+    r.rot = rot;
+    r.wide_positions = t.position_bits == 64;
+    r.neighbours = interleaved;
+    r.w_dtype = w_dtype;
+    r.eps = eps;
+    r.inv_dim = 1.0 / (double)dim;
+    return r;
+}
 
 int done(hipError_t e, const char *what) { return e == hipSuccess ? OPT_OK : report_hip(e, what); }
 
@@ -257,6 +346,220 @@ int opt_block_matmul(const opt_product *n, void *stream)
     a.accumulate = add;
     a.exact = !(n->accumulate & OPT_CODE_PRODUCTS);
     return done(launch_block_matmul(n->c_dtype, a, (hipStream_t)stream), "block product launch");
+}
+
+int opt_gated_act(const opt_gate *n, void *stream)
+{
+    int rc;
+    if (!n) return report(OPT_EINVAL, "the argument record is NULL");
+    if ((rc = check_dtype(n->dtype, "dtype")) != OPT_OK) return rc;
+    if ((rc = check_act(n->act)) != OPT_OK) return rc;
+    if ((rc = check_sides(n->rows, n->cols)) != OPT_OK) return rc;
+    if (n->rows == 0 || n->cols == 0) return OPT_OK;
+    if (!n->y && !n->q.codes && !n->gate_q.codes && !n->up_q.codes) return report(OPT_EINVAL, "no output is given");
+    const size_t size = size_of(n->dtype);
+    if ((rc = check_matrix("gate", n->gate, n->ldg, n->rows, n->cols, size)) != OPT_OK) return rc;
+    if ((rc = check_matrix("up", n->up, n->ldu, n->rows, n->cols, size)) != OPT_OK) return rc;
+    if ((rc = check_more("y", n->y, n->ldy, n->rows, n->cols, size)) != OPT_OK) return rc;
+    if ((rc = check_more("q", n->q, n->rows, n->cols)) != OPT_OK) return rc;
+    if ((rc = check_more("gate_q", n->gate_q, n->rows, n->cols)) != OPT_OK) return rc;
+    if ((rc = check_more("up_q", n->up_q, n->rows, n->cols)) != OPT_OK) return rc;
+    GateArgs a{};
+    a.rows = n->rows;
+    a.cols = n->cols;
+    a.gate = n->gate;
+    a.up = n->up;
+    a.y = n->y;
+    a.ldg = n->ldg;
+    a.ldu = n->ldu;
+    a.ldy = n->ldy;
+    a.q = codes_of(n->q);
+    a.gq = codes_of(n->gate_q);
+    a.uq = codes_of(n->up_q);
+    return done(launch_gated_act(n->dtype, n->act, a, (hipStream_t)stream), "gated activation launch");
+}
+
+int opt_gated_act_backward(const opt_gate_grad *n, void *stream)
+{
+    int rc;
+    if (!n) return report(OPT_EINVAL, "the argument record is NULL");
+    if ((rc = check_dtype(n->dtype, "dtype")) != OPT_OK) return rc;
+    if ((rc = check_act(n->act)) != OPT_OK) return rc;
+    if ((rc = check_sides(n->rows, n->cols)) != OPT_OK) return rc;
+    if (n->rows == 0 || n->cols == 0) return OPT_OK;
+    if (!n->dgate && !n->dup && !n->dgate_q.codes && !n->dup_q.codes && !n->dgate_t.codes && !n->dup_t.codes && !n->y_t.codes)
+        return report(OPT_EINVAL, "no output is given");
+    const size_t size = size_of(n->dtype);
+    if ((rc = check_matrix("dy", n->dy, n->lddy, n->rows, n->cols, size)) != OPT_OK) return rc;
+    if (n->gate || n->up) {
+        if (n->gate_q.codes || n->up_q.codes) return report(OPT_EINVAL, "gate and up are given as matrices or as codes, not both");
+        if ((rc = check_matrix("gate", n->gate, n->ldg, n->rows, n->cols, size)) != OPT_OK) return rc;
+        if ((rc = check_matrix("up", n->up, n->ldu, n->rows, n->cols, size)) != OPT_OK) return rc;
+    } else {
+        if ((rc = check_codes("gate_q", n->gate_q, n->rows, n->cols)) != OPT_OK) return rc;
+        if ((rc = check_codes("up_q", n->up_q, n->rows, n->cols)) != OPT_OK) return rc;
+    }
+    if ((rc = check_more("dgate", n->dgate, n->lddg, n->rows, n->cols, size)) != OPT_OK) return rc;
+    if ((rc = check_more("dup", n->dup, n->lddu, n->rows, n->cols, size)) != OPT_OK) return rc;
+    if (n->dgate && n->dgate == n->dup) return report(OPT_EINVAL, "dgate and dup must be different matrices");
+    if ((rc = check_more("dgate_q", n->dgate_q, n->rows, n->cols)) != OPT_OK) return rc;
+    if ((rc = check_more("dup_q", n->dup_q, n->rows, n->cols)) != OPT_OK) return rc;
+    if ((rc = check_more("dgate_t", n->dgate_t, n->cols, n->rows)) != OPT_OK) return rc;
+    if ((rc = check_more("dup_t", n->dup_t, n->cols, n->rows)) != OPT_OK) return rc;
+    if ((rc = check_more("y_t", n->y_t, n->cols, n->rows)) != OPT_OK) return rc;
+    GateGradArgs a{};
+    a.rows = n->rows;
+    a.cols = n->cols;
+    a.dy = n->dy;
+    a.gate = n->gate;
+    a.up = n->up;
+    a.dgate = n->dgate;
+    a.dup = n->dup;
+    a.lddy = n->lddy;
+    a.ldg = n->ldg;
+    a.ldu = n->ldu;
+    a.lddg = n->lddg;
+    a.lddu = n->lddu;
+    a.gq = codes_of(n->gate_q);
+    a.uq = codes_of(n->up_q);
+    a.dgq = codes_of(n->dgate_q);
+    a.duq = codes_of(n->dup_q);
+    a.dgt = codes_of(n->dgate_t);
+    a.dut = codes_of(n->dup_t);
+    a.yt = codes_of(n->y_t);
+    return done(launch_gated_act_grad(n->dtype, n->act, a, (hipStream_t)stream), "gated activation backward launch");
+}
+
+int opt_block_restore(const opt_restore *n, void *stream)
+{
+    int rc;
+    if (!n) return report(OPT_EINVAL, "the argument record is NULL");
+    if ((rc = check_dtype(n->dtype, "dtype")) != OPT_OK) return rc;
+    if ((rc = check_sides(n->rows, n->cols)) != OPT_OK) return rc;
+    if (n->rows == 0 || n->cols == 0) return OPT_OK;
+    if (!n->x && !n->qt.codes) return report(OPT_EINVAL, "neither x nor qt is given");
+    if ((rc = check_codes("q", n->q, n->rows, n->cols)) != OPT_OK) return rc;
+    if ((rc = check_more("x", n->x, n->ldx, n->rows, n->cols, size_of(n->dtype))) != OPT_OK) return rc;
+    if ((rc = check_more("qt", n->qt, n->cols, n->rows)) != OPT_OK) return rc;
+    if (n->qt.codes == n->q.codes) return report(OPT_EINVAL, "q and qt must be different matrices");
+    RestoreArgs a{};
+    a.rows = n->rows;
+    a.cols = n->cols;
+    a.q = codes_of(n->q);
+    a.x = n->x;
+    a.ldx = n->ldx;
+    a.qt = codes_of(n->qt);
+    return done(launch_block_restore(n->dtype, a, (hipStream_t)stream), "block restore launch");
+}
+
+int opt_head_norm(const opt_heads *n, void *stream)
+{
+    int rc;
+    if (!n) return report(OPT_EINVAL, "the argument record is NULL");
+    if ((rc = check_turn(n->tokens, n->dim, n->rot, n->dtype, n->w_dtype, n->interleaved, n->eps)) != OPT_OK) return rc;
+    HeadArgs a{};
+    int64_t heads = 0;
+    for (int i = 0; i < 2; ++i) {
+        const opt_head_set &s = i ? n->k : n->q;
+        const char *const names[2][4] = {{"q", "q's x", "q's y", "q's weight"}, {"k", "k's x", "k's y", "k's weight"}};
+        if ((rc = check_count(names[i][0], s.heads, n->tokens, s.codes.codes != nullptr)) != OPT_OK) return rc;
+        heads += s.heads;
+        if (s.heads == 0 || n->tokens == 0) continue;
+        const size_t size = size_of(n->dtype);
+        if ((rc = check_heads(names[i][1], s.x, s.x_token, s.x_head, n->tokens, s.heads, n->dim, size, false)) != OPT_OK) return rc;
+        if ((rc = check_heads(names[i][2], s.y, s.y_token, s.y_head, n->tokens, s.heads, n->dim, size, true)) != OPT_OK) return rc;
+        if ((rc = check_more(names[i][3], s.weight, n->dim, 1, n->dim, size_of(n->w_dtype))) != OPT_OK) return rc;
+        if ((rc = check_more(names[i][0], s.codes, n->tokens * s.heads, n->dim)) != OPT_OK) return rc;
+        HeadSet &d = a.s[i];
+        d.heads = s.heads;
+        d.x = s.x;
+        d.w = s.weight;
+        d.y = s.y;
+        d.xt = s.x_token;
+        d.xh = s.x_head;
+        d.yt = s.y_token;
+        d.yh = s.y_head;
+        d.q = codes_of(s.codes);
+    }
+    if (n->tokens == 0 || heads == 0) return OPT_OK;
+    if ((rc = check_table(n->table, n->tokens, n->rot)) != OPT_OK) return rc;
+    a.t = turn_of(n->tokens, n->dim, n->rot, n->w_dtype, n->interleaved, n->eps, n->table);
+    return done(launch_head_norm(n->dtype, a, (hipStream_t)stream), "head norm launch");
+}
+
+int64_t opt_head_norm_workspace(int64_t tokens, int64_t heads_q, int64_t heads_k, int32_t dim)
+{
+    int rc;
+    if (tokens < 0 || tokens >= kMaxSide) return report(OPT_EINVAL, "tokens must lie in [0, 2^31)");
+    if ((rc = check_count("q", heads_q, tokens, false)) != OPT_OK) return rc;
+    if ((rc = check_count("k", heads_k, tokens, false)) != OPT_OK) return rc;
+    if (dim < 1) return report(OPT_EINVAL, "dim must be positive");
+    if (dim > kMaxHeadDim) return report(OPT_EUNSUPPORTED, "heads above %d elements", kMaxHeadDim);
+    if (tokens == 0 || heads_q + heads_k == 0) return 0;
+    return head_grad_groups(tokens, heads_q, heads_k, dim) * 2 * dim * (int64_t)sizeof(float);
+}
+
+int opt_head_norm_backward(const opt_heads_grad *n, void *stream)
+{
+    int rc;
+    if (!n) return report(OPT_EINVAL, "the argument record is NULL");
+    if ((rc = check_turn(n->tokens, n->dim, n->rot, n->dtype, n->w_dtype, n->interleaved, n->eps)) != OPT_OK) return rc;
+    if (n->accumulate != 0 && n->accumulate != 1) return report(OPT_EINVAL, "accumulate must be 0 or 1");
+    HeadGradArgs a{};
+    int64_t heads = 0, coded = 0, plain = 0;
+    for (int i = 0; i < 2; ++i) {
+        const opt_head_grad_set &s = i ? n->k : n->q;
+        const char *const names[2][5] = {{"q", "q's x", "q's dy", "q's dx", "q's weight"}, {"k", "k's x", "k's dy", "k's dx", "k's weight"}};
+        if ((rc = check_count(names[i][0], s.heads, n->tokens, !s.x)) != OPT_OK) return rc;
+        if (s.dweight && !at(s.dweight, 4)) return report(OPT_EALIGN, "dweight must be 4-byte aligned");
+        heads += s.heads;
+        if (s.heads == 0 || n->tokens == 0) continue;
+        const size_t size = size_of(n->dtype);
+        if (s.x && s.codes.codes) return report(OPT_EINVAL, "%s is given as a matrix or as codes, not both", names[i][1]);
+        if (s.x) {
+            ++plain;
+            if ((rc = check_heads(names[i][1], s.x, s.x_token, s.x_head, n->tokens, s.heads, n->dim, size, false)) != OPT_OK) return rc;
+        } else {
+            ++coded;
+            if ((rc = check_codes(names[i][1], s.codes, n->tokens * s.heads, n->dim)) != OPT_OK) return rc;
+        }
+        if ((rc = check_heads(names[i][2], s.dy, s.dy_token, s.dy_head, n->tokens, s.heads, n->dim, size, false)) != OPT_OK) return rc;
+        if ((rc = check_heads(names[i][3], s.dx, s.dx_token, s.dx_head, n->tokens, s.heads, n->dim, size, true)) != OPT_OK) return rc;
+        if (s.dx == s.x) return report(OPT_EINVAL, "dx and x must be different");
+        if ((rc = check_more(names[i][4], s.weight, n->dim, 1, n->dim, size_of(n->w_dtype))) != OPT_OK) return rc;
+        HeadGradSet &d = a.s[i];
+        d.heads = s.heads;
+        d.dy = s.dy;
+        d.x = s.x;
+        d.w = s.weight;
+        d.dx = s.dx;
+        d.dyt = s.dy_token;
+        d.dyh = s.dy_head;
+        d.xt = s.x_token;
+        d.xh = s.x_head;
+        d.dxt = s.dx_token;
+        d.dxh = s.dx_head;
+        d.q = codes_of(s.codes);
+    }
+    if (coded && plain) return report(OPT_EINVAL, "q and k are both given as matrices or both as codes");
+    if (n->q.dweight && n->q.dweight == n->k.dweight) return report(OPT_EINVAL, "the two dweights must be different");
+    const bool any = n->tokens > 0 && heads > 0, sums = n->q.dweight || n->k.dweight;
+    if (any) {
+        if ((rc = check_table(n->table, n->tokens, n->rot)) != OPT_OK) return rc;
+        if (sums) {
+            const int64_t need = head_grad_groups(n->tokens, n->q.heads, n->k.heads, n->dim) * 2 * n->dim * (int64_t)sizeof(float);
+            if (!n->workspace) return report(OPT_EINVAL, "dweight needs a workspace");
+            if (!at(n->workspace, 16)) return report(OPT_EALIGN, "the workspace must be 16-byte aligned");
+            if (n->workspace_bytes < need)
+                return report(OPT_EINVAL, "the workspace has %lld bytes of %lld", (long long)n->workspace_bytes, (long long)need);
+        }
+    } else if (!sums) {
+        return OPT_OK;
+    }
+    a.t = turn_of(n->tokens, n->dim, n->rot, n->w_dtype, n->interleaved, n->eps, n->table);
+    a.part = any && sums ? (float *)n->workspace : nullptr;
+    return done(launch_head_norm_grad(n->dtype, coded > 0, a, n->q.dweight, n->k.dweight, n->accumulate, (hipStream_t)stream),
+                "head norm backward launch");
 }
 
 }  // extern "C"

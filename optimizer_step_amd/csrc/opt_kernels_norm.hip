@@ -19,56 +19,6 @@
 
 namespace optstep {
 
-__device__ __forceinline__ double two_words(uint32_t lo, uint32_t hi) { return __hiloint2double((int)hi, (int)lo); }
-
-template <int CTRL>
-__device__ __forceinline__ double dpp_add(double x)
-{
-    const uint32_t lo = (uint32_t)__double2loint(x), hi = (uint32_t)__double2hiint(x);
-    return x + two_words((uint32_t)__builtin_amdgcn_mov_dpp((int)lo, CTRL, 0xF, 0xF, true),
-                         (uint32_t)__builtin_amdgcn_mov_dpp((int)hi, CTRL, 0xF, 0xF, true));
-}
-
-// Sum over 16 or 64 lanes, the same bits in every lane: each step adds two
-// partial sums that both sides hold (lanes 1, 2, 7 - i and 15 - i away by DPP;
-// then the rows and the halves of the wave by gfx950's lane swaps).
-template <int LANES>
-__device__ __forceinline__ double lanes_sum(double x)
-{
-    x = dpp_add<0xB1>(x);
-    x = dpp_add<0x4E>(x);
-    x = dpp_add<0x141>(x);
-    x = dpp_add<0x140>(x);
-    if (LANES >= 64) {
-        uint32_t lo = (uint32_t)__double2loint(x), hi = (uint32_t)__double2hiint(x);
-        auto l = __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
-        auto h = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
-        x = two_words(l[0], h[0]) + two_words(l[1], h[1]);
-        lo = (uint32_t)__double2loint(x);
-        hi = (uint32_t)__double2hiint(x);
-        l = __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
-        h = __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
-        x = two_words(l[0], h[0]) + two_words(l[1], h[1]);
-    }
-    return x;
-}
-
-// 1/sqrt(x) to within 2^-51: the hardware's estimate and two Newton steps, a
-// tenth of the instructions of a division after a square root (each of which
-// every wave would run once a row: 33 -> 31 us of a pass over 8192 x 4096).
-// Where a step has no value (x zero or infinite) the estimate is the result.
-__device__ __forceinline__ double inverse_root(double x)
-{
-    const double y0 = __builtin_amdgcn_rsq(x);
-    double y = y0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const double e = __builtin_fma(-x * y, y, 1.0);
-        y = __builtin_fma(0.5 * y, e, y);
-    }
-    return y == y ? y : y0;
-}
-
 constexpr int norm_threads(int lanes) { return lanes < 256 ? 256 : lanes; }
 
 // The sums of a row over its LANES lanes, in every lane.  Waves meet in `slot`

@@ -64,6 +64,76 @@ struct MatmulArgs {
     int exact;             // 0: a 16-bit c may take the 8-bit products
 };
 
+constexpr int kActSilu = 0, kActGelu = 1;
+constexpr int kMaxHeadDim = 512;   // longest head (a head stays in a wave's registers)
+
+struct GateArgs {
+    int64_t rows, cols;
+    const void *gate, *up;
+    void *y;
+    int64_t ldg, ldu, ldy;
+    Codes q, gq, uq;       // codes null: not written
+};
+
+struct GateGradArgs {
+    int64_t rows, cols;
+    const void *dy, *gate, *up;    // gate null: from gq and uq
+    void *dgate, *dup;
+    int64_t lddy, ldg, ldu, lddg, lddu;
+    Codes gq, uq;
+    Codes dgq, duq, dgt, dut, yt;  // codes null: not written
+};
+
+struct RestoreArgs {
+    int64_t rows, cols;
+    Codes q;
+    void *x;               // null: not written
+    int64_t ldx;
+    Codes qt;              // codes null: not written
+};
+
+// The queries or the keys of a call (strides in elements).
+struct HeadSet {
+    int64_t heads;
+    const void *x, *w;
+    void *y;
+    int64_t xt, xh, yt, yh;
+    Codes q;
+};
+
+struct HeadGradSet {
+    int64_t heads;
+    const void *dy, *x, *w;        // x null: from q
+    void *dx;
+    int64_t dyt, dyh, xt, xh, dxt, dxh;
+    Codes q;
+};
+
+// What both passes of the heads share.
+struct HeadTurn {
+    int64_t tokens, table_rows, ldt;
+    const float *table;
+    const void *positions; // null: token t stands at row t
+    int dim, rot;
+    int wide_positions;    // 64-bit
+    int neighbours;        // pairs (2 i, 2 i + 1), not (i, i + rot/2)
+    int w_dtype;
+    double eps, inv_dim;
+};
+
+struct HeadArgs {
+    HeadTurn t;
+    HeadSet s[2];
+};
+
+struct HeadGradArgs {
+    HeadTurn t;
+    HeadGradSet s[2];
+    float *part;           // [groups][2][dim] partial sums of the weights' gradients, or null
+};
+
+int64_t head_grad_groups(int64_t tokens, int64_t heads_q, int64_t heads_k, int dim);
+
 // Lanes of a row and workgroups of the norm's backward pass, by the shape
 // alone (so that the weight gradient's order of addition is too).
 struct NormShape {
@@ -224,6 +294,57 @@ __device__ __forceinline__ void load8_any(int dt, const void *p, int64_t j, int 
 
 __device__ __forceinline__ int left8(int64_t j, int64_t end) { return end - j >= 8 ? 8 : end > j ? (int)(end - j) : 0; }
 
+__device__ __forceinline__ double two_words(uint32_t lo, uint32_t hi) { return __hiloint2double((int)hi, (int)lo); }
+
+template <int CTRL>
+__device__ __forceinline__ double dpp_add(double x)
+{
+    const uint32_t lo = (uint32_t)__double2loint(x), hi = (uint32_t)__double2hiint(x);
+    return x + two_words((uint32_t)__builtin_amdgcn_mov_dpp((int)lo, CTRL, 0xF, 0xF, true),
+                         (uint32_t)__builtin_amdgcn_mov_dpp((int)hi, CTRL, 0xF, 0xF, true));
+}
+
+// Sum over 8, 16, 32 or 64 lanes, the same bits in every lane: each step adds
+// two partial sums that both sides hold (lanes 1, 2, 7 - i and 15 - i away by
+// DPP; then the rows and the halves of the wave by gfx950's lane swaps).
+template <int LANES>
+__device__ __forceinline__ double lanes_sum(double x)
+{
+    x = dpp_add<0xB1>(x);
+    x = dpp_add<0x4E>(x);
+    x = dpp_add<0x141>(x);
+    if (LANES >= 16) x = dpp_add<0x140>(x);
+    if (LANES >= 32) {
+        const uint32_t lo = (uint32_t)__double2loint(x), hi = (uint32_t)__double2hiint(x);
+        const auto l = __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+        const auto h = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+        x = two_words(l[0], h[0]) + two_words(l[1], h[1]);
+    }
+    if (LANES >= 64) {
+        const uint32_t lo = (uint32_t)__double2loint(x), hi = (uint32_t)__double2hiint(x);
+        const auto l = __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
+        const auto h = __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+        x = two_words(l[0], h[0]) + two_words(l[1], h[1]);
+    }
+    return x;
+}
+
+// 1/sqrt(x) to within 2^-51: the hardware's estimate and two Newton steps, a
+// tenth of the instructions of a division after a square root (each of which
+// every wave would run once a row: 33 -> 31 us of a pass over 8192 x 4096).
+// Where a step has no value (x zero or infinite) the estimate is the result.
+__device__ __forceinline__ double inverse_root(double x)
+{
+    const double y0 = __builtin_amdgcn_rsq(x);
+    double y = y0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const double e = __builtin_fma(-x * y, y, 1.0);
+        y = __builtin_fma(0.5 * y, e, y);
+    }
+    return y == y ? y : y0;
+}
+
 // Largest of the 16 lanes of a row (every lane ends with it): the first steps
 // of wave_max_u32.
 __device__ __forceinline__ uint32_t row16_max_u32(uint32_t v)
@@ -273,6 +394,36 @@ __device__ __forceinline__ u2 encode8(const float v[8], uint32_t byte)
     if (byte == 255u) return (u2){0u, 0u};    // a NaN block's codes are zeros: its scale says NaN
     const float inv = block_inverse(byte);
     return (u2){encode4(v[0], v[1], v[2], v[3], inv), encode4(v[4], v[5], v[6], v[7], inv)};
+}
+
+// Eight values of a block-coded row as two words of codes, and the block's
+// scale: exact where the product is a binary32 number.
+__device__ __forceinline__ float block_value(uint32_t byte)
+{
+    return byte == 255u ? bitsf(0x7FC00000u) : byte == 0u ? bitsf(0x00400000u) : bitsf(byte << 23);
+}
+
+__device__ __forceinline__ void decode8(u2 code, float scale, float v[8])
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const f2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)code[i], false);
+        const f2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)code[i], true);
+        v[4 * i] = lo[0] * scale;
+        v[4 * i + 1] = lo[1] * scale;
+        v[4 * i + 2] = hi[0] * scale;
+        v[4 * i + 3] = hi[1] * scale;
+    }
+}
+
+// Largest of a lane's value and those 16 and 32 lanes away: of the four rows
+// of a wave, in every lane.
+__device__ __forceinline__ uint32_t rows_max_u32(uint32_t v)
+{
+    auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max(p[0], p[1]);
+    p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return max(p[0], p[1]);
 }
 
 }  // namespace optstep
