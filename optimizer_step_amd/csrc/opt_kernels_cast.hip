@@ -13,6 +13,16 @@
 
 namespace optstep {
 
+// Largest of a lane's value and those 16 and 32 lanes away: of the four rows
+// of a wave, in every lane.
+__device__ __forceinline__ uint32_t rows_max_u32(uint32_t v)
+{
+    auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max(p[0], p[1]);
+    p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return max(p[0], p[1]);
+}
+
 // Where the codes of rows 8 g .. 8 g + 7 of a column sit in the transposed
 // tile: 16 lanes that write the same rows of columns eight apart, and 8 that
 // read one column's, each fall into different banks.

@@ -9,22 +9,27 @@
 
 namespace optstep {
 
-// sigma(p) and 1 - sigma(p), each to a few binary32 units of itself: both come
-// from e = exp(-|p|) <= 1, so neither overflows nor cancels.  FINE: the rounding
-// of |p| log2(e), which exp2 would make relative |p| 2^-24 of e, is carried
-// along (|p| held at 256, where e is 0, so that it is finite); 16-bit and 8-bit
-// results do not see it.  A NaN p may give any values: its x makes them NaN.
+// sigma(p) and 1 - sigma(p).  FINE (32-bit results): each to a few binary32
+// units of itself.  Both come from e = exp(-|p|) <= 1, so neither overflows nor
+// cancels, and the rounding of |p| log2(e), which exp2 would make relative |p|
+// 2^-24 of e, is carried along (|p| held at 256, where e is 0, so that it is
+// finite).  16-bit and 8-bit results do not see those: there exp(-p) may reach
+// infinity, where sigma is 0, and 1 - sigma is good to 2^-23 of 1.  A NaN p may
+// give any values: its x makes them NaN.
 template <bool FINE>
 __device__ __forceinline__ void logistic(float p, float &sig, float &rest)
 {
-    const float a = FINE ? __builtin_fminf(__builtin_fabsf(p), 256.0f) : __builtin_fabsf(p);
+    if (!FINE) {
+        sig = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(p * -1.44269504f));
+        rest = 1.0f - sig;
+        return;
+    }
+    const float a = __builtin_fminf(__builtin_fabsf(p), 256.0f);
     const float t = a * -1.44269504f;
     float e = __builtin_amdgcn_exp2f(t);
-    if (FINE) {
-        // -a log2(e) = t + (its rounding + a times what the constant lacks)
-        const float lo = __builtin_fmaf(a, -1.92596299e-8f, __builtin_fmaf(a, -1.44269504f, -t));
-        e = __builtin_fmaf(e * 0.693147181f, lo, e);
-    }
+    // -a log2(e) = t + (its rounding + a times what the constant lacks)
+    const float lo = __builtin_fmaf(a, -1.92596299e-8f, __builtin_fmaf(a, -1.44269504f, -t));
+    e = __builtin_fmaf(e * 0.693147181f, lo, e);
     const float big = __builtin_amdgcn_rcpf(1.0f + e), small = e * big;
     sig = p >= 0.0f ? big : small;
     rest = p >= 0.0f ? small : big;
@@ -67,17 +72,17 @@ __device__ __forceinline__ void act_slope(float x, float &s, float &slope)
 }
 
 // One row's block of 128 columns by 16 lanes: codes and the scale's byte.
-__device__ __forceinline__ void put_block(const Codes &q, int64_t row, int64_t c, bool live, int64_t cols16, const float v[8])
+__device__ __forceinline__ uint32_t put_block(const Codes &q, int64_t row, int64_t c, bool live, int64_t cols16, const float v[8])
 {
-    const uint32_t byte = block_scale(row16_max_u32(abs_max8(v)));
-    const u2 code = encode8(v, byte);
+    const uint32_t byte = block_scale(row16_max_u32(top8(v)));
+    const u2 code = codes8(v, byte);
     if (live && c < cols16) gst<u2>(q.codes + row * q.ld + c, code);
-    if (live && (threadIdx.x & 15) == 0) gst<uint8_t>(q.scales + (c / kCodeBlock) * q.lds + row, (uint8_t)byte);
+    return byte;
 }
 
 constexpr int kGateRows = 16;      // rows of a workgroup's tile of 128 columns
 
-template <int DT, int ACT>
+template <int DT, int ACT, bool EIGHTS>
 __global__ __launch_bounds__(256) void gated_act_kernel(GateArgs a)
 {
     const int64_t tc = (a.cols + 127) / 128, tiles = tc * ((a.rows + kGateRows - 1) / kGateRows);
@@ -87,26 +92,139 @@ __global__ __launch_bounds__(256) void gated_act_kernel(GateArgs a)
         const bool live = row < a.rows;
         const int cnt = live ? left8(c, a.cols) : 0;
         float g[8], u[8], y[8];
-        load8<DT>(a.gate, row * a.ldg + c, cnt, g);
-        load8<DT>(a.up, row * a.ldu + c, cnt, u);
+        load8<DT, EIGHTS>(a.gate, row * a.ldg + c, cnt, g);
+        load8<DT, EIGHTS>(a.up, row * a.ldu + c, cnt, u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = act<ACT, DT == kP32>(g[i]) * u[i];
-        if (a.y) store8<DT>(a.y, row * a.ldy + c, cnt, y);
-        if (a.q.codes) put_block(a.q, row, c, live, cols16, y);
-        if (a.gq.codes) put_block(a.gq, row, c, live, cols16, g);
-        if (a.uq.codes) put_block(a.uq, row, c, live, cols16, u);
+        if (a.y) store8<DT, EIGHTS>(a.y, row * a.ldy + c, cnt, y);
+        const Codes *const q[3] = {&a.q, &a.gq, &a.uq};
+        const float *const v[3] = {y, g, u};
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            if (!q[j]->codes) continue;
+            const uint32_t byte = put_block(*q[j], row, c, live, cols16, v[j]);
+            if (live && (threadIdx.x & 15) == 0) gst<uint8_t>(q[j]->scales + (c / kCodeBlock) * q[j]->lds + row, (uint8_t)byte);
+        }
+    }
+}
+
+// The backward pass where no transpose is coded: dgate, dup and their codes, by
+// rows.
+template <int DT, int ACT, bool CODED, bool EIGHTS>
+__global__ __launch_bounds__(256) void gated_act_grad_rows_kernel(GateGradArgs a)
+{
+    const int64_t tc = (a.cols + 127) / 128, tiles = tc * ((a.rows + kGateRows - 1) / kGateRows);
+    const int64_t cols16 = (a.cols + 15) & ~(int64_t)15;
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int64_t row = (t / tc) * kGateRows + threadIdx.x / 16, c = (t % tc) * 128 + 8 * (threadIdx.x & 15);
+        const bool live = row < a.rows;
+        const int cnt = live ? left8(c, a.cols) : 0;
+        float g[8], u[8], d[8], v[2][8];
+        load8<DT, EIGHTS>(a.dy, row * a.lddy + c, cnt, d);
+        if (CODED) {
+            const Codes *const in[2] = {&a.gq, &a.uq};
+            float *const out[2] = {g, u};
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                u2 code = {0u, 0u};
+                uint32_t byte = 0;
+                if (cnt > 0) {
+                    code = gld<u2>(in[n]->codes + row * in[n]->ld + c);
+                    byte = gld<uint8_t>(in[n]->scales + (c / kCodeBlock) * in[n]->lds + row);
+                }
+                decode8(code, byte, out[n]);
+            }
+        } else {
+            load8<DT, EIGHTS>(a.gate, row * a.ldg + c, cnt, g);
+            load8<DT, EIGHTS>(a.up, row * a.ldu + c, cnt, u);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            float s, slope;
+            act_slope<ACT, DT == kP32>(g[k], s, slope);
+            v[0][k] = d[k] * u[k] * slope;
+            v[1][k] = d[k] * s;
+            // columns past the last: a scale that says NaN makes NaNs of their zero codes
+            if (CODED && !EIGHTS && k >= cnt) v[0][k] = v[1][k] = 0.0f;
+        }
+        if (a.dgate) store8<DT, EIGHTS>(a.dgate, row * a.lddg + c, cnt, v[0]);
+        if (a.dup) store8<DT, EIGHTS>(a.dup, row * a.lddu + c, cnt, v[1]);
+        const Codes *const q[2] = {&a.dgq, &a.duq};
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            if (!q[n]->codes) continue;
+            const uint32_t byte = put_block(*q[n], row, c, live, cols16, v[n]);
+            if (live && (threadIdx.x & 15) == 0) gst<uint8_t>(q[n]->scales + (c / kCodeBlock) * q[n]->lds + row, (uint8_t)byte);
+        }
     }
 }
 
 // ---- tiles of 128 x 128 whose transpose is coded too -----------------------
 // 512 threads: thread t holds the eight columns of group t % 16 in the four
-// rows of group t / 16.
+// rows of group t / 16.  N matrices at once share the barriers.
 
 constexpr int kTileThreads = 512;
 
+// A kernel's argument record where the launch left it.  A record of many
+// matrices held in scalar registers spills them; read again where it is used
+// (again() forgets what was read) it costs a scalar load.
+#if defined(__HIP_DEVICE_COMPILE__)
+#define OPT_CONST __attribute__((address_space(4)))
+#else
+#define OPT_CONST
+#endif
+
+template <class A>
+__device__ __forceinline__ const OPT_CONST A *kernargs() { return (const OPT_CONST A *)__builtin_amdgcn_kernarg_segment_ptr(); }
+
+template <class A>
+__device__ __forceinline__ const OPT_CONST A *again(const OPT_CONST A *a)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+s"(a));
+#endif
+    return a;
+}
+
+__device__ __forceinline__ Codes copy(const OPT_CONST Codes &q) { return Codes{q.codes, q.ld, q.scales, q.lds}; }
+
+// The wave's number, in a scalar register.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6); }
+
+// Where a thread's four rows of a tile begin: the address of the wave's first
+// row is scalar work, a lane adds its group's distance from it.
+struct Spot {
+    char *p;
+    int64_t step;          // bytes from a row to the next
+    __device__ __forceinline__ char *row(int i) const { return p + i * step; }
+};
+
+template <int SIZE>
+__device__ __forceinline__ Spot spot(const void *base, int64_t ld, int64_t r0, int64_t c0)
+{
+    const int64_t step = ld * SIZE;
+    char *p = (char *)base + (r0 + 16 * wave_id()) * step + c0 * SIZE;
+    return Spot{p + (int64_t)(threadIdx.x >> 4 & 3) * (4 * step) + (threadIdx.x & 15) * (8 * SIZE), step};
+}
+
+// How many of a thread's four rows exist, and of its eight columns.
+__device__ __forceinline__ int rows_of(int64_t rows, int64_t r0)
+{
+    const int left = (int)(rows - r0 < 128 ? rows - r0 : 128) - 4 * (int)(threadIdx.x >> 4);
+    return left < 0 ? 0 : left > 4 ? 4 : left;
+}
+
+__device__ __forceinline__ int cols_of(int64_t cols, int64_t c0)
+{
+    const int left = (int)(cols - c0 < 128 ? cols - c0 : 128) - 8 * (int)(threadIdx.x & 15);
+    return left < 0 ? 0 : left > 8 ? 8 : left;
+}
+
+template <int N>
 struct TileLds {
-    uint32_t cmax[8][128];                                       // largest magnitude of a column in a wave's 16 rows
-    __attribute__((aligned(16))) uint8_t tr[128 * 128];          // codes by column
+    uint32_t top[N][128];                                        // a column's largest magnitude, then its scale as a binary32 word
+    uint32_t lost;                                               // a column that holds a NaN or an infinity
+    __attribute__((aligned(16))) uint8_t tr[N][128 * 128];       // codes by column
 };
 
 // Where the codes of rows 4 g .. 4 g + 3 of a column sit: the 16-byte chunk
@@ -114,129 +232,290 @@ struct TileLds {
 // of columns eight apart fall into different banks.
 __device__ __forceinline__ int quad_at(int col, int g) { return col * 128 + 16 * ((g >> 2) ^ (col >> 3 & 7)) + 4 * (g & 3); }
 
-// Codes of the transpose of the tile at (r0, c0): column c of the tile is row
-// c0 + c of the coded matrix, its 128 rows one block.  Every thread calls it.
-__device__ __forceinline__ void put_transposed(TileLds &lds, const Codes &q, int64_t r0, int64_t c0, int64_t rows, int64_t cols,
-                                               const float (&v)[4][8])
+// Before any thread's add_tops, with a barrier after it.
+template <int N>
+__device__ __forceinline__ void clear_tops(TileLds<N> &lds)
 {
-    const int cl = threadIdx.x & 15, rg = threadIdx.x >> 4, wave = threadIdx.x >> 6;
-    uint32_t m[8];
+    if (threadIdx.x < N * 128) lds.top[0][threadIdx.x] = 0;
+    if (threadIdx.x == 0) lds.lost = 0;
+}
+
+// Largest over the four rows of a wave of four columns' values, one column a
+// row: each swap brings two columns together, each maximum halves their rows.
+__device__ __forceinline__ uint32_t four_columns(const uint32_t m[4])
+{
+    const auto a = __builtin_amdgcn_permlane16_swap(m[0], m[1], false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(m[2], m[3], false, false);
+    const auto c = __builtin_amdgcn_permlane32_swap(max(a[0], a[1]), max(b[0], b[1]), false, false);
+    return max(c[0], c[1]);
+}
+
+// A thread's largest magnitudes of its eight columns join the tile's.
+__device__ __forceinline__ void add_tops(uint32_t (&top)[128], const float m[8])
+{
+    uint32_t b[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        m[k] = 0;
+    for (int k = 0; k < 8; ++k) b[k] = fbits(m[k]) & 0x7FFFFFFFu;
+    uint32_t *const at = top + 8 * (threadIdx.x & 15) + (threadIdx.x >> 4 & 3);
+    atomicMax(at, four_columns(b));
+    atomicMax(at + 4, four_columns(b + 4));
+}
+
+// The scale of one column for each of 128 threads, to the LDS and to the coded
+// transpose at (c0 + column, block of row r0); between two barriers.
+template <int N>
+__device__ __forceinline__ void set_scale(TileLds<N> &lds, int n, const Codes &q, int64_t r0, int64_t c0, int64_t cols)
+{
+    const int col = threadIdx.x % 128;
+    const uint32_t byte = block_scale(lds.top[n][col]);
+    lds.top[n][col] = byte << 23;
+    if (byte == 255u) lds.lost = 1;
+    if (c0 + col < cols) gst<uint8_t>(q.scales + (r0 / 128) * q.lds + c0 + col, (uint8_t)byte);
+}
+
+// Codes of a thread's four rows of column `col` of its group's eight, whose
+// scale is the binary32 word x.
+__device__ __forceinline__ void put_column(uint8_t *tr, int k, uint32_t x, bool lost, float a, float b, float c, float d)
+{
+    uint32_t code = codes4(a, b, c, d, x);
+    if (lost) code = x == 255u << 23 ? 0u : code;
+    *(uint32_t *)(tr + quad_at(8 * (threadIdx.x & 15) + k, threadIdx.x >> 4)) = code;
+}
+
+// The coded transpose of a tile goes out of the LDS.
+__device__ __forceinline__ void put_tile(const uint8_t *tr, const Codes &q, int64_t r0, int64_t c0, int64_t rows, int64_t cols)
+{
+    const int cols_left = (int)(cols - c0 < 128 ? cols - c0 : 128), rows_left = (int)(rows - r0 < 128 ? rows - r0 : 128);
+    const int col = threadIdx.x >> 3, g = threadIdx.x & 7;      // 16 codes of a column
+    char *const base = (char *)q.codes + (c0 + 8 * wave_id()) * q.ld + r0;
+    char *const at = base + (int64_t)(col & 7) * q.ld + 16 * g;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m[k] = max(m[k], fbits(v[i][k]) & 0x7FFFFFFFu);
-        m[k] = rows_max_u32(m[k]);
+    for (int i = 0; i < 2; ++i)
+        if (col + 64 * i < cols_left && 16 * g < rows_left) gst<u4>(at + 64 * i * q.ld, *(const u4 *)(tr + quad_at(col + 64 * i, 4 * g)));
+}
+
+// A thread's eight columns in its four rows of a coded matrix's tile, as they
+// are stored (zeros where it has none; code rows are padded to 16 with zero
+// codes, a block's scales to 4 rows).
+struct CodedRows { u2 code[4]; uint32_t bytes; };
+
+__device__ __forceinline__ CodedRows load_coded(const Codes &q, int64_t r0, int64_t c0, int live)
+{
+    const Spot at = spot<1>(q.codes, q.ld, r0, c0);
+    CodedRows x;
+    x.bytes = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x.code[i] = (u2){0u, 0u};
+        if (i < live) x.code[i] = gld<u2>(at.row(i));
     }
-    __syncthreads();               // what the last call left in the LDS is read
-    if ((threadIdx.x & 63) < 16) {
-        *(u4 *)&lds.cmax[wave][8 * cl] = (u4){m[0], m[1], m[2], m[3]};
-        *(u4 *)&lds.cmax[wave][8 * cl + 4] = (u4){m[4], m[5], m[6], m[7]};
-    }
-    __syncthreads();
+    if (live > 0) x.bytes = gld<uint32_t>(q.scales + (c0 / kCodeBlock) * q.lds + r0 + 4 * (threadIdx.x >> 4));
+    return x;
+}
+
+// Half of a thread's eight columns: four values.
+__device__ __forceinline__ void half_of(const CodedRows &q, int i, int h, float v[4])
+{
+    const float x = bitsf((q.bytes >> (8 * i) & 255u) << 23);
+    const f2_t lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q.code[i][h], x, false);
+    const f2_t hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q.code[i][h], x, true);
+    v[0] = lo[0];
+    v[1] = lo[1];
+    v[2] = hi[0];
+    v[3] = hi[1];
+}
+
+template <int DT>
+struct RawRows { Raw<DT> row[4]; };
+
+template <int DT>
+__device__ __forceinline__ void half_of(const RawRows<DT> &q, int i, int h, float v[4])
+{
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        uint32_t top = lds.cmax[0][8 * cl + k];
-#pragma unroll
-        for (int w = 1; w < 8; ++w) top = max(top, lds.cmax[w][8 * cl + k]);
-        const uint32_t byte = block_scale(top);
-        const float inv = block_inverse(byte);
-        const uint32_t code = byte == 255u ? 0u : encode4(v[0][k], v[1][k], v[2][k], v[3][k], inv);
-        *(uint32_t *)(lds.tr + quad_at(8 * cl + k, rg)) = code;
-        if (rg == k && c0 + 8 * cl + k < cols) gst<uint8_t>(q.scales + (r0 / 128) * q.lds + c0 + 8 * cl + k, (uint8_t)byte);
-    }
-    __syncthreads();
-    const int64_t rows16 = (rows + 15) & ~(int64_t)15;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int col = (threadIdx.x >> 3) + 64 * i, g = threadIdx.x & 7;      // 16 codes of a column
-        if (c0 + col < cols && r0 + 16 * g < rows16)
-            gst<u4>(q.codes + (c0 + col) * q.ld + r0 + 16 * g, *(const u4 *)(lds.tr + quad_at(col, 4 * g)));
+    for (int j = 0; j < 4; ++j) {
+        if (DT == kP32) {
+            v[j] = bitsf(q.row[i].v[h & (DT == kP32)][j]);
+        } else {
+            const uint32_t w = q.row[i].v[0][2 * h + (j >> 1)];
+            v[j] = DT == kPBF16 ? (j & 1 ? bf16_hi(w) : bf16_lo(w)) : (j & 1 ? f16_hi(w) : f16_lo(w));
+        }
     }
 }
 
-// Eight columns of a row of a coded matrix (zeros where it has none; code rows
-// are padded to 16 with zero codes).
-__device__ __forceinline__ void load_coded(const Codes &q, int64_t row, int64_t c, bool there, float v[8])
+template <int DT, bool EIGHTS>
+__device__ __forceinline__ RawRows<DT> load_rows(const void *p, int64_t ld, int64_t r0, int64_t c0, int live, int have)
 {
-    u2 code = {0u, 0u};
-    uint32_t byte = 127u;
-    if (there) {
-        code = gld<u2>(q.codes + row * q.ld + c);
-        byte = gld<uint8_t>(q.scales + (c / kCodeBlock) * q.lds + row);
-    }
-    decode8(code, block_value(byte), v);
+    const Spot at = spot<sizeof(typename Elem<DT>::T)>(p, ld, r0, c0);
+    RawRows<DT> x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x.row[i] = load_raw<DT, EIGHTS>(at.row(i), 0, i < live ? have : 0);
+    return x;
 }
 
-template <int DT, int ACT, bool CODED>
-__global__ __launch_bounds__(kTileThreads) void gated_act_grad_kernel(GateGradArgs a)
+// Forgets what was computed from these registers.
+__device__ __forceinline__ void hold(CodedRows &q)
 {
-    __shared__ TileLds lds;
-    constexpr bool kFine = DT == kP32;
-    const int cl = threadIdx.x & 15, rg = threadIdx.x >> 4;
-    const int64_t tc = (a.cols + 127) / 128, tiles = tc * ((a.rows + 127) / 128);
-    const int64_t cols16 = (a.cols + 15) & ~(int64_t)15;
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int64_t r0 = (t / tc) * 128, c0 = (t % tc) * 128;
-        const int64_t c = c0 + 8 * cl, r = r0 + 4 * rg;
-        const int have = left8(c, a.cols);
-        float dg[4][8], du[4][8], y[4][8];
+    asm volatile("" : "+v"(q.code[0]), "+v"(q.code[1]), "+v"(q.code[2]), "+v"(q.code[3]), "+v"(q.bytes));
+}
+
+template <int DT>
+__device__ __forceinline__ void hold(RawRows<DT> &q)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        asm volatile("" : "+v"(q.row[i].v[0]));
+        if (DT == kP32) asm volatile("" : "+v"(q.row[i].v[DT == kP32]));
+    }
+}
+
+// One of dgate (WHAT 0), dup (1) and y (2), of four columns of row i.
+// Columns past the last are zeros (a scale that says NaN makes NaNs of their
+// zero codes).
+template <int DT, int ACT, bool CODED, bool EIGHTS, int WHAT, class In>
+__device__ __forceinline__ void grad4(const In &g, const In &u, const RawRows<DT> &d, int i, int h, int cnt, float v[4])
+{
+    float gv[4], uv[4], dv[4];
+    half_of(g, i, h, gv);
+    if (WHAT != 1) half_of(u, i, h, uv);
+    if (WHAT != 2) half_of(d, i, h, dv);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float s, slope;
+        act_slope<ACT, DT == kP32>(gv[k], s, slope);
+        v[k] = WHAT == 0 ? dv[k] * uv[k] * slope : WHAT == 1 ? dv[k] * s : s * uv[k];
+        if (CODED && !EIGHTS && 4 * h + k >= cnt) v[k] = 0.0f;
+    }
+}
+
+template <bool CODED, int DT> struct GateIn { typedef CodedRows T; };
+template <int DT> struct GateIn<false, DT> { typedef RawRows<DT> T; };
+
+// All outputs of one of the three matrices of a tile.
+template <int DT, int ACT, bool CODED, bool EIGHTS, int WHAT, class In>
+__device__ __forceinline__ void grad_part(const OPT_CONST GateGradArgs *a, TileLds<3> &lds, In &g, In &u, RawRows<DT> &d, int64_t r0, int64_t c0)
+{
+    a = again(a);
+    void *const m = WHAT == 0 ? a->dgate : WHAT == 1 ? a->dup : nullptr;
+    const Codes q = WHAT == 0 ? copy(a->dgq) : WHAT == 1 ? copy(a->duq) : Codes{}, qt = copy(WHAT == 0 ? a->dgt : WHAT == 1 ? a->dut : a->yt);
+    if (!m && !q.codes && !qt.codes) return;
+    const int have = cols_of(a->cols, c0), live = rows_of(a->rows, r0);
+    hold(g);
+    hold(u);
+    hold(d);
+    float v[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) grad4<DT, ACT, CODED, EIGHTS, WHAT>(g, u, d, i, h, i < live ? have : 0, v[i] + 4 * h);
+    if (m) {
+        const Spot at = spot<sizeof(typename Elem<DT>::T)>(m, WHAT == 0 ? a->lddg : a->lddu, r0, c0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store8<DT, EIGHTS>(at.row(i), 0, i < live ? have : 0, v[i]);
+    }
+    if (qt.codes) {
+        float top[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top[k] = __builtin_elementwise_maximum(max_abs(v[0][k], v[1][k]), max_abs(v[2][k], v[3][k]));
+        add_tops(lds.top[WHAT], top);
+    }
+    if (q.codes) {
+        const Spot at = spot<1>(q.codes, q.ld, r0, c0);
+        const bool padded = cols_of((a->cols + 15) & ~(int64_t)15, c0) > 0;
+        uint32_t mine = 0;             // lane i of a row keeps row i's scale: one store for the four
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t row = r + i;
-            const bool live = row < a.rows;
-            const int cnt = live ? have : 0;
-            float g[8], u[8], d[8];
-            load8<DT>(a.dy, row * a.lddy + c, cnt, d);
-            if (CODED) {
-                load_coded(a.gq, row, c, cnt > 0, g);
-                load_coded(a.uq, row, c, cnt > 0, u);
-            } else {
-                load8<DT>(a.gate, row * a.ldg + c, cnt, g);
-                load8<DT>(a.up, row * a.ldu + c, cnt, u);
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float s, slope;
-                act_slope<ACT, kFine>(g[k], s, slope);
-                // columns past the last one: a scale of infinity or NaN would make NaNs of their zero codes
-                const bool in = k < cnt;
-                dg[i][k] = in ? d[k] * u[k] * slope : 0.0f;
-                du[i][k] = in ? d[k] * s : 0.0f;
-                y[i][k] = in ? s * u[k] : 0.0f;
-            }
-            if (a.dgate) store8<DT>(a.dgate, row * a.lddg + c, cnt, dg[i]);
-            if (a.dup) store8<DT>(a.dup, row * a.lddu + c, cnt, du[i]);
-            if (a.dgq.codes) put_block(a.dgq, row, c, live, cols16, dg[i]);
-            if (a.duq.codes) put_block(a.duq, row, c, live, cols16, du[i]);
+            const uint32_t byte = block_scale(row16_max_u32(top8(v[i])));
+            const u2 code = codes8(v[i], byte);
+            if (i < live && padded) gst<u2>(at.row(i), code);
+            if ((threadIdx.x & 15) == i) mine = byte;
         }
-        if (a.dgt.codes) put_transposed(lds, a.dgt, r0, c0, a.rows, a.cols, dg);
-        if (a.dut.codes) put_transposed(lds, a.dut, r0, c0, a.rows, a.cols, du);
-        if (a.yt.codes) put_transposed(lds, a.yt, r0, c0, a.rows, a.cols, y);
+        if ((int)(threadIdx.x & 15) < live)
+            gst<uint8_t>(q.scales + (c0 / kCodeBlock) * q.lds + r0 + 4 * (threadIdx.x >> 4) + (threadIdx.x & 15), (uint8_t)mine);
+    }
+    if (!qt.codes) return;
+    __syncthreads();
+    if (threadIdx.x < 128) set_scale(lds, WHAT, qt, r0, c0, a->cols);
+    __syncthreads();
+    const bool lost = lds.lost != 0;
+    const u4 x0 = *(const u4 *)(lds.top[WHAT] + 8 * (threadIdx.x & 15)), x1 = *(const u4 *)(lds.top[WHAT] + 8 * (threadIdx.x & 15) + 4);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) put_column(lds.tr[WHAT], k, k < 4 ? x0[k & 3] : x1[k & 3], lost, v[0][k], v[1][k], v[2][k], v[3][k]);
+}
+
+template <int DT, int ACT, bool CODED, bool EIGHTS>
+__global__ __launch_bounds__(kTileThreads, DT == kP32 && !CODED ? 2 : 4) void gated_act_grad_kernel(GateGradArgs)
+{
+    __shared__ TileLds<3> lds;
+    const OPT_CONST GateGradArgs *a = kernargs<GateGradArgs>();
+    for (int64_t r0 = (int64_t)blockIdx.y * 128; r0 < a->rows; r0 += (int64_t)gridDim.y * 128)
+    for (int64_t c0 = (int64_t)blockIdx.x * 128; c0 < a->cols; c0 += (int64_t)gridDim.x * 128) {
+        a = again(a);
+        const int have = cols_of(a->cols, c0), live = rows_of(a->rows, r0);
+        typename GateIn<CODED, DT>::T g, u;
+        if constexpr (CODED) {
+            g = load_coded(copy(a->gq), r0, c0, have > 0 ? live : 0);
+            u = load_coded(copy(a->uq), r0, c0, have > 0 ? live : 0);
+        } else {
+            g = load_rows<DT, EIGHTS>(a->gate, a->ldg, r0, c0, live, have);
+            u = load_rows<DT, EIGHTS>(a->up, a->ldu, r0, c0, live, have);
+        }
+        RawRows<DT> d = load_rows<DT, EIGHTS>(a->dy, a->lddy, r0, c0, live, have);
+        clear_tops(lds);
+        __syncthreads();
+        // the three one after the other, each from the inputs: all at once would take 96 registers for the values alone
+        grad_part<DT, ACT, CODED, EIGHTS, 0>(a, lds, g, u, d, r0, c0);
+        grad_part<DT, ACT, CODED, EIGHTS, 1>(a, lds, g, u, d, r0, c0);
+        grad_part<DT, ACT, CODED, EIGHTS, 2>(a, lds, g, u, d, r0, c0);
+        __syncthreads();
+        a = again(a);
+        if (a->dgt.codes) put_tile(lds.tr[0], copy(a->dgt), r0, c0, a->rows, a->cols);
+        if (a->dut.codes) put_tile(lds.tr[1], copy(a->dut), r0, c0, a->rows, a->cols);
+        if (a->yt.codes) put_tile(lds.tr[2], copy(a->yt), r0, c0, a->rows, a->cols);
     }
 }
 
 // Values of a coded matrix, and codes of its transpose.
-template <int DT>
-__global__ __launch_bounds__(kTileThreads) void block_restore_kernel(RestoreArgs a)
+template <int DT, bool EIGHTS>
+__global__ __launch_bounds__(kTileThreads) void block_restore_kernel(RestoreArgs)
 {
-    __shared__ TileLds lds;
-    const int cl = threadIdx.x & 15, rg = threadIdx.x >> 4;
-    const int64_t tc = (a.cols + 127) / 128, tiles = tc * ((a.rows + 127) / 128);
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int64_t r0 = (t / tc) * 128, c0 = (t % tc) * 128;
-        const int64_t c = c0 + 8 * cl, r = r0 + 4 * rg;
-        const int have = left8(c, a.cols);
+    __shared__ TileLds<1> lds;
+    const OPT_CONST RestoreArgs *a = kernargs<RestoreArgs>();
+    for (int64_t r0 = (int64_t)blockIdx.y * 128; r0 < a->rows; r0 += (int64_t)gridDim.y * 128)
+    for (int64_t c0 = (int64_t)blockIdx.x * 128; c0 < a->cols; c0 += (int64_t)gridDim.x * 128) {
+        const int have = cols_of(a->cols, c0), live = rows_of(a->rows, r0);
+        const CodedRows q = load_coded(copy(a->q), r0, c0, have > 0 ? live : 0);
+        const bool transposed = a->qt.codes;
+        if (transposed) {
+            clear_tops(lds);
+            __syncthreads();
+        }
         float v[4][8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int cnt = r + i < a.rows ? have : 0;
-            load_coded(a.q, r + i, c, cnt > 0, v[i]);
+            decode8(q.code[i], q.bytes >> (8 * i) & 255u, v[i]);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[i][k] = k < cnt ? v[i][k] : 0.0f;
-            if (a.x) store8<DT>(a.x, (r + i) * a.ldx + c, cnt, v[i]);
+            for (int k = 0; k < 8; ++k)
+                if (!EIGHTS && k >= (i < live ? have : 0)) v[i][k] = 0.0f;
         }
-        if (a.qt.codes) put_transposed(lds, a.qt, r0, c0, a.rows, a.cols, v);
+        if (a->x) {
+            const Spot at = spot<sizeof(typename Elem<DT>::T)>(a->x, a->ldx, r0, c0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) store8<DT, EIGHTS>(at.row(i), 0, i < live ? have : 0, v[i]);
+        }
+        if (!transposed) continue;
+        float top[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top[k] = __builtin_elementwise_maximum(max_abs(v[0][k], v[1][k]), max_abs(v[2][k], v[3][k]));
+        add_tops(lds.top[0], top);
+        __syncthreads();
+        if (threadIdx.x < 128) set_scale(lds, 0, copy(a->qt), r0, c0, a->cols);
+        __syncthreads();
+        const bool lost = lds.lost != 0;
+        const u4 x0 = *(const u4 *)(lds.top[0] + 8 * (threadIdx.x & 15)), x1 = *(const u4 *)(lds.top[0] + 8 * (threadIdx.x & 15) + 4);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) put_column(lds.tr[0], k, k < 4 ? x0[k & 3] : x1[k & 3], lost, v[0][k], v[1][k], v[2][k], v[3][k]);
+        __syncthreads();
+        put_tile(lds.tr[0], copy(a->qt), r0, c0, a->rows, a->cols);
     }
 }
 
@@ -244,28 +523,49 @@ __global__ __launch_bounds__(kTileThreads) void block_restore_kernel(RestoreArgs
 
 static unsigned grid_of(int64_t tiles) { return (unsigned)(tiles < (1 << 20) ? tiles : 1 << 20); }
 
+// Tiles of 128 x 128: a workgroup each, of at most 2^20 (and 2^10 down).
+static dim3 tiles_of(int64_t rows, int64_t cols)
+{
+    const int64_t x = (cols + 127) / 128, y = (rows + 127) / 128, most = (int64_t)1 << 20;
+    const int64_t gy = y < 1024 ? y : 1024;
+    return dim3((unsigned)(x < most / gy ? x : most / gy), (unsigned)gy);
+}
+
 template <int DT, int ACT>
 static hipError_t launch_gate_t(const GateArgs &a, hipStream_t st)
 {
     const int64_t tiles = ((a.cols + 127) / 128) * ((a.rows + kGateRows - 1) / kGateRows);
-    hipLaunchKernelGGL((gated_act_kernel<DT, ACT>), dim3(grid_of(tiles)), dim3(256), 0, st, a);
+    if (a.cols % 8 == 0) hipLaunchKernelGGL((gated_act_kernel<DT, ACT, true>), dim3(grid_of(tiles)), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((gated_act_kernel<DT, ACT, false>), dim3(grid_of(tiles)), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+template <int DT, int ACT, bool CODED, bool EIGHTS>
+static hipError_t launch_gate_grad_t(const GateGradArgs &a, hipStream_t st)
+{
+    if (a.dgt.codes || a.dut.codes || a.yt.codes) {
+        hipLaunchKernelGGL((gated_act_grad_kernel<DT, ACT, CODED, EIGHTS>), tiles_of(a.rows, a.cols), dim3(kTileThreads), 0, st, a);
+    } else {
+        const int64_t tiles = ((a.cols + 127) / 128) * ((a.rows + kGateRows - 1) / kGateRows);
+        hipLaunchKernelGGL((gated_act_grad_rows_kernel<DT, ACT, CODED, EIGHTS>), dim3(grid_of(tiles)), dim3(256), 0, st, a);
+    }
     return hipGetLastError();
 }
 
 template <int DT, int ACT>
-static hipError_t launch_gate_grad_t(const GateGradArgs &a, hipStream_t st)
+static hipError_t launch_gate_grad_a(const GateGradArgs &a, hipStream_t st)
 {
-    const unsigned grid = grid_of(((a.cols + 127) / 128) * ((a.rows + 127) / 128));
-    if (a.gate) hipLaunchKernelGGL((gated_act_grad_kernel<DT, ACT, false>), dim3(grid), dim3(kTileThreads), 0, st, a);
-    else hipLaunchKernelGGL((gated_act_grad_kernel<DT, ACT, true>), dim3(grid), dim3(kTileThreads), 0, st, a);
-    return hipGetLastError();
+    const bool eights = a.cols % 8 == 0;
+    if (a.gate) return eights ? launch_gate_grad_t<DT, ACT, false, true>(a, st) : launch_gate_grad_t<DT, ACT, false, false>(a, st);
+    return eights ? launch_gate_grad_t<DT, ACT, true, true>(a, st) : launch_gate_grad_t<DT, ACT, true, false>(a, st);
 }
 
 template <int DT>
 static hipError_t launch_restore_t(const RestoreArgs &a, hipStream_t st)
 {
-    const unsigned grid = grid_of(((a.cols + 127) / 128) * ((a.rows + 127) / 128));
-    hipLaunchKernelGGL((block_restore_kernel<DT>), dim3(grid), dim3(kTileThreads), 0, st, a);
+    const dim3 grid = tiles_of(a.rows, a.cols);
+    if (a.cols % 8 == 0) hipLaunchKernelGGL((block_restore_kernel<DT, true>), grid, dim3(kTileThreads), 0, st, a);
+    else hipLaunchKernelGGL((block_restore_kernel<DT, false>), grid, dim3(kTileThreads), 0, st, a);
     return hipGetLastError();
 }
 
@@ -278,9 +578,9 @@ hipError_t launch_gated_act(int dt, int act, const GateArgs &a, hipStream_t st)
 
 hipError_t launch_gated_act_grad(int dt, int act, const GateGradArgs &a, hipStream_t st)
 {
-    if (dt == kP32) return act == kActSilu ? launch_gate_grad_t<kP32, kActSilu>(a, st) : launch_gate_grad_t<kP32, kActGelu>(a, st);
-    if (dt == kPBF16) return act == kActSilu ? launch_gate_grad_t<kPBF16, kActSilu>(a, st) : launch_gate_grad_t<kPBF16, kActGelu>(a, st);
-    return act == kActSilu ? launch_gate_grad_t<kPF16, kActSilu>(a, st) : launch_gate_grad_t<kPF16, kActGelu>(a, st);
+    if (dt == kP32) return act == kActSilu ? launch_gate_grad_a<kP32, kActSilu>(a, st) : launch_gate_grad_a<kP32, kActGelu>(a, st);
+    if (dt == kPBF16) return act == kActSilu ? launch_gate_grad_a<kPBF16, kActSilu>(a, st) : launch_gate_grad_a<kPBF16, kActGelu>(a, st);
+    return act == kActSilu ? launch_gate_grad_a<kPF16, kActSilu>(a, st) : launch_gate_grad_a<kPF16, kActGelu>(a, st);
 }
 
 hipError_t launch_block_restore(int dt, const RestoreArgs &a, hipStream_t st)

@@ -164,8 +164,8 @@ __global__ __launch_bounds__(kHeadThreads) void head_norm_kernel(HeadArgs a, int
             }
             store8<DT, MODE == kHalves>(s.y, token * s.yt + head * s.yh + c, n, y);
             if (s.q.codes) {
-                const uint32_t byte = block_scale(block_max_u32<L>(abs_max8(x)));
-                const u2 code = encode8(x, byte);
+                const uint32_t byte = block_scale(block_max_u32<L>(top8(x)));
+                const u2 code = codes8(x, byte);
                 const int64_t line = token * s.heads + head;
                 if (live && c < ((t.dim + 15) & ~15)) gst<u2>(s.q.codes + line * s.q.ld + c, code);
                 if (n > 0 && (lane & 15) == 0) gst<uint8_t>(s.q.scales + (c / kCodeBlock) * s.q.lds + line, (uint8_t)byte);
@@ -207,7 +207,7 @@ __global__ __launch_bounds__(kHeadThreads) void head_norm_grad_kernel(HeadGradAr
                     code = gld<u2>(s.q.codes + line * s.q.ld + c);
                     byte = gld<uint8_t>(s.q.scales + (c / kCodeBlock) * s.q.lds + line);
                 }
-                decode8(code, block_value(byte), x);
+                decode8(code, byte, x);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = i < n ? x[i] : 0.0f;
             } else {

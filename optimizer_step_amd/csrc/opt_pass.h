@@ -396,34 +396,53 @@ __device__ __forceinline__ u2 encode8(const float v[8], uint32_t byte)
     return (u2){encode4(v[0], v[1], v[2], v[3], inv), encode4(v[4], v[5], v[6], v[7], inv)};
 }
 
-// Eight values of a block-coded row as two words of codes, and the block's
-// scale: exact where the product is a binary32 number.
-__device__ __forceinline__ float block_value(uint32_t byte)
+// The same codes by gfx950's scaled conversions, which divide by the power of
+// two X (given as a binary32 word, the scale's byte in its exponent) on the way:
+// equal to encode4's on every block that is not NaN, at half its instructions.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, uint32_t x)
 {
-    return byte == 255u ? bitsf(0x7FC00000u) : byte == 0u ? bitsf(0x00400000u) : bitsf(byte << 23);
+    typedef short pair __attribute__((ext_vector_type(2)));
+    pair w = {0, 0};
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, bitsf(x), false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, bitsf(x), true);
+    return __builtin_bit_cast(uint32_t, w);
 }
 
-__device__ __forceinline__ void decode8(u2 code, float scale, float v[8])
+__device__ __forceinline__ u2 codes8(const float v[8], uint32_t byte)
 {
+    const u2 w = {codes4(v[0], v[1], v[2], v[3], byte << 23), codes4(v[4], v[5], v[6], v[7], byte << 23)};
+    return byte == 255u ? (u2){0u, 0u} : w;
+}
+
+// Eight values of a block-coded row, from its codes and their scale's byte:
+// code times 2^(byte - 127), exact where that is a binary32 number; NaN for 255.
+__device__ __forceinline__ void decode8(u2 code, uint32_t byte, float v[8])
+{
+    const float x = bitsf(byte << 23);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const f2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)code[i], false);
-        const f2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)code[i], true);
-        v[4 * i] = lo[0] * scale;
-        v[4 * i + 1] = lo[1] * scale;
-        v[4 * i + 2] = hi[0] * scale;
-        v[4 * i + 3] = hi[1] * scale;
+        const f2_t lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(code[i], x, false);
+        const f2_t hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(code[i], x, true);
+        v[4 * i] = lo[0];
+        v[4 * i + 1] = lo[1];
+        v[4 * i + 2] = hi[0];
+        v[4 * i + 3] = hi[1];
     }
 }
 
-// Largest of a lane's value and those 16 and 32 lanes away: of the four rows
-// of a wave, in every lane.
-__device__ __forceinline__ uint32_t rows_max_u32(uint32_t v)
+// Bits of the largest magnitude of eight values, a NaN's if one is NaN: the
+// maximum that propagates NaNs takes three operands and their magnitudes at once.
+__device__ __forceinline__ float max_abs(float a, float b)
 {
-    auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    v = max(p[0], p[1]);
-    p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    return max(p[0], p[1]);
+    return __builtin_elementwise_maximum(__builtin_fabsf(a), __builtin_fabsf(b));
+}
+
+__device__ __forceinline__ uint32_t top8(const float v[8])
+{
+    float m = max_abs(v[0], v[1]);
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) m = __builtin_elementwise_maximum(m, max_abs(v[i], v[i + 1]));
+    return fbits(m) & 0x7FFFFFFFu;
 }
 
 }  // namespace optstep

@@ -53,8 +53,10 @@ def gate_gradients(dy, x, u, act, dtype):
     sig, rest = logistic(p)
     e = loss(p, act, dtype)
     s, tail = x * sig, x * sig * rest * dp
-    # s rest p': sigma's and rest's errors, the products, p' to 4 units; sigma's own; their sum; two products
-    size = np.abs(tail) * (2 * e + 8 * U) + sig * (e + 2 * U) + 3 * U * np.abs(sig + tail)
+    # s rest p': sigma's and rest's errors, the products, p' to 4 units; sigma's own; their sum; two products.
+    # 16-bit types form rest as 1 - sigma: off by what sigma is off, and a rounding below 1
+    of_rest = np.abs(tail) * e if dtype == "f32" else np.abs(x * sig * dp) * (sig * e + U)
+    size = np.abs(tail) * (e + 8 * U) + of_rest + sig * (e + 2 * U) + 3 * U * np.abs(sig + tail)
     dg, du = dy * u * (sig + tail), dy * s
     tiny = FLUSH * (1 + np.abs(x)) * (1 + np.abs(dp))
     return ((dg, np.abs(dy * u) * (size + tiny)), (du, np.abs(du) * (e + 2 * U) + np.abs(dy) * tiny),
