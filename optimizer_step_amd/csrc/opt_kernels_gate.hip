@@ -68,16 +68,16 @@ __device__ __forceinline__ void act_slope(float x, float &s, float &slope)
     inner<ACT>(x, p, dp);
     logistic<FINE>(p, sig, rest);
     s = x * sig;
-    slope = __builtin_fmaf(s * rest, dp, sig);
+    slope = ACT == kActSilu ? __builtin_fmaf(s, rest, sig) : __builtin_fmaf(s * rest, dp, sig);
 }
 
 // One row's block of 128 columns by 16 lanes: codes and the scale's byte.
-__device__ __forceinline__ uint32_t put_block(const Codes &q, int64_t row, int64_t c, bool live, int64_t cols16, const float v[8])
+__device__ __forceinline__ void put_block(const Codes &q, int64_t row, int64_t c, bool live, int64_t cols16, const float v[8])
 {
-    const uint32_t byte = block_scale(row16_max_u32(top8(v)));
-    const u2 code = codes8(v, byte);
-    if (live && c < cols16) gst<u2>(q.codes + row * q.ld + c, code);
-    return byte;
+    uint32_t word;
+    const u2 code = code_block(v, row16_max_u32(top8(v)), word);
+    if (live && c < cols16) sst<u2>(q.codes + row * q.ld + c, code);
+    if (live && (threadIdx.x & 15) == 0) gst<uint8_t>(q.scales + (c / kCodeBlock) * q.lds + row, (uint8_t)(word >> 23));
 }
 
 constexpr int kGateRows = 16;      // rows of a workgroup's tile of 128 columns
@@ -101,9 +101,7 @@ __global__ __launch_bounds__(256) void gated_act_kernel(GateArgs a)
         const float *const v[3] = {y, g, u};
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
-            if (!q[j]->codes) continue;
-            const uint32_t byte = put_block(*q[j], row, c, live, cols16, v[j]);
-            if (live && (threadIdx.x & 15) == 0) gst<uint8_t>(q[j]->scales + (c / kCodeBlock) * q[j]->lds + row, (uint8_t)byte);
+            if (q[j]->codes) put_block(*q[j], row, c, live, cols16, v[j]);
         }
     }
 }
@@ -152,9 +150,7 @@ __global__ __launch_bounds__(256) void gated_act_grad_rows_kernel(GateGradArgs a
         const Codes *const q[2] = {&a.dgq, &a.duq};
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-            if (!q[n]->codes) continue;
-            const uint32_t byte = put_block(*q[n], row, c, live, cols16, v[n]);
-            if (live && (threadIdx.x & 15) == 0) gst<uint8_t>(q[n]->scales + (c / kCodeBlock) * q[n]->lds + row, (uint8_t)byte);
+            if (q[n]->codes) put_block(*q[n], row, c, live, cols16, v[n]);
         }
     }
 }
@@ -164,6 +160,10 @@ __global__ __launch_bounds__(256) void gated_act_grad_rows_kernel(GateGradArgs a
 // rows of group t / 16.  N matrices at once share the barriers.
 
 constexpr int kTileThreads = 512;
+
+// What a kernel knows of its matrix.  kFull: sides that are multiples of 128,
+// so that every tile is whole.  kEights: columns a multiple of eight.
+enum { kAnyShape = 0, kEights = 1, kFull = 2 };
 
 // A kernel's argument record where the launch left it.  A record of many
 // matrices held in scalar registers spills them; read again where it is used
@@ -207,23 +207,27 @@ __device__ __forceinline__ Spot spot(const void *base, int64_t ld, int64_t r0, i
     return Spot{p + (int64_t)(threadIdx.x >> 4 & 3) * (4 * step) + (threadIdx.x & 15) * (8 * SIZE), step};
 }
 
-// How many of a thread's four rows exist, and of its eight columns.
+// How many of a thread's four rows exist, and of its eight columns (of a whole tile: all).
+template <int SHAPE>
 __device__ __forceinline__ int rows_of(int64_t rows, int64_t r0)
 {
+    if (SHAPE == kFull) return 4;
     const int left = (int)(rows - r0 < 128 ? rows - r0 : 128) - 4 * (int)(threadIdx.x >> 4);
     return left < 0 ? 0 : left > 4 ? 4 : left;
 }
 
+template <int SHAPE>
 __device__ __forceinline__ int cols_of(int64_t cols, int64_t c0)
 {
+    if (SHAPE == kFull) return 8;
     const int left = (int)(cols - c0 < 128 ? cols - c0 : 128) - 8 * (int)(threadIdx.x & 15);
     return left < 0 ? 0 : left > 8 ? 8 : left;
 }
 
 template <int N>
 struct TileLds {
-    uint32_t top[N][128];                                        // a column's largest magnitude, then its scale as a binary32 word
-    uint32_t lost;                                               // a column that holds a NaN or an infinity
+    uint32_t top[N][128];                                        // bits of a column's largest magnitude, then its scale's word
+    uint32_t lost;                                               // a column holds a NaN or an infinity
     __attribute__((aligned(16))) uint8_t tr[N][128 * 128];       // codes by column
 };
 
@@ -232,7 +236,7 @@ struct TileLds {
 // of columns eight apart fall into different banks.
 __device__ __forceinline__ int quad_at(int col, int g) { return col * 128 + 16 * ((g >> 2) ^ (col >> 3 & 7)) + 4 * (g & 3); }
 
-// Before any thread's add_tops, with a barrier after it.
+// Before any thread's add_tops, with a barrier between.
 template <int N>
 __device__ __forceinline__ void clear_tops(TileLds<N> &lds)
 {
@@ -251,47 +255,54 @@ __device__ __forceinline__ uint32_t four_columns(const uint32_t m[4])
 }
 
 // A thread's largest magnitudes of its eight columns join the tile's.
-__device__ __forceinline__ void add_tops(uint32_t (&top)[128], const float m[8])
+__device__ __forceinline__ void add_tops(uint32_t (&top)[128], const float (&v)[4][8])
 {
     uint32_t b[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) b[k] = fbits(m[k]) & 0x7FFFFFFFu;
+    for (int k = 0; k < 8; ++k) b[k] = fbits(__builtin_elementwise_maximum(max_abs(v[0][k], v[1][k]), max_abs(v[2][k], v[3][k])));
     uint32_t *const at = top + 8 * (threadIdx.x & 15) + (threadIdx.x >> 4 & 3);
     atomicMax(at, four_columns(b));
     atomicMax(at + 4, four_columns(b + 4));
 }
 
-// The scale of one column for each of 128 threads, to the LDS and to the coded
-// transpose at (c0 + column, block of row r0); between two barriers.
+// Between two barriers: the scales of the tile's columns, to the LDS and to the
+// coded transpose; 128 threads, so that the others' columns cost them nothing.
 template <int N>
-__device__ __forceinline__ void set_scale(TileLds<N> &lds, int n, const Codes &q, int64_t r0, int64_t c0, int64_t cols)
+__device__ __forceinline__ void set_scales(TileLds<N> &lds, int n, const Codes &q, int64_t r0, int64_t c0, int64_t cols)
 {
-    const int col = threadIdx.x % 128;
-    const uint32_t byte = block_scale(lds.top[n][col]);
-    lds.top[n][col] = byte << 23;
+    if (threadIdx.x >= 128) return;
+    const uint32_t byte = block_scale(lds.top[n][threadIdx.x]);
+    lds.top[n][threadIdx.x] = byte << 23;
     if (byte == 255u) lds.lost = 1;
-    if (c0 + col < cols) gst<uint8_t>(q.scales + (r0 / 128) * q.lds + c0 + col, (uint8_t)byte);
+    if (c0 + threadIdx.x < cols) gst<uint8_t>(q.scales + (r0 / 128) * q.lds + c0 + threadIdx.x, (uint8_t)byte);
 }
 
-// Codes of a thread's four rows of column `col` of its group's eight, whose
-// scale is the binary32 word x.
-__device__ __forceinline__ void put_column(uint8_t *tr, int k, uint32_t x, bool lost, float a, float b, float c, float d)
+// The tile's codes to the LDS, by column (a lost column's are put right on the
+// way out).
+template <int N>
+__device__ __forceinline__ void code_columns(TileLds<N> &lds, int n, const float (&v)[4][8])
 {
-    uint32_t code = codes4(a, b, c, d, x);
-    if (lost) code = x == 255u << 23 ? 0u : code;
-    *(uint32_t *)(tr + quad_at(8 * (threadIdx.x & 15) + k, threadIdx.x >> 4)) = code;
+    const int cl = threadIdx.x & 15;
+    const u4 x0 = *(const u4 *)(lds.top[n] + 8 * cl), x1 = *(const u4 *)(lds.top[n] + 8 * cl + 4);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        *(uint32_t *)(lds.tr[n] + quad_at(8 * cl + k, threadIdx.x >> 4)) = codes4(v[0][k], v[1][k], v[2][k], v[3][k], k < 4 ? x0[k & 3] : x1[k & 3]);
 }
 
 // The coded transpose of a tile goes out of the LDS.
-__device__ __forceinline__ void put_tile(const uint8_t *tr, const Codes &q, int64_t r0, int64_t c0, int64_t rows, int64_t cols)
+template <int SHAPE, int N>
+__device__ __forceinline__ void put_tile(const TileLds<N> &lds, int n, const Codes &q, int64_t r0, int64_t c0, int64_t rows, int64_t cols)
 {
     const int cols_left = (int)(cols - c0 < 128 ? cols - c0 : 128), rows_left = (int)(rows - r0 < 128 ? rows - r0 : 128);
     const int col = threadIdx.x >> 3, g = threadIdx.x & 7;      // 16 codes of a column
-    char *const base = (char *)q.codes + (c0 + 8 * wave_id()) * q.ld + r0;
-    char *const at = base + (int64_t)(col & 7) * q.ld + 16 * g;
+    char *const at = (char *)q.codes + (c0 + 8 * wave_id()) * q.ld + r0 + (int64_t)(col & 7) * q.ld + 16 * g;
+    const bool lost = lds.lost != 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (col + 64 * i < cols_left && 16 * g < rows_left) gst<u4>(at + 64 * i * q.ld, *(const u4 *)(tr + quad_at(col + 64 * i, 4 * g)));
+    for (int i = 0; i < 2; ++i) {
+        u4 code = *(const u4 *)(lds.tr[n] + quad_at(col + 64 * i, 4 * g));
+        if (lost && lds.top[n][col + 64 * i] == kLostWord) code = (u4){0u, 0u, 0u, 0u};
+        if (SHAPE == kFull || (col + 64 * i < cols_left && 16 * g < rows_left)) gst<u4>(at + 64 * i * q.ld, code);
+    }
 }
 
 // A thread's eight columns in its four rows of a coded matrix's tile, as they
@@ -342,13 +353,13 @@ __device__ __forceinline__ void half_of(const RawRows<DT> &q, int i, int h, floa
     }
 }
 
-template <int DT, bool EIGHTS>
+template <int DT, int SHAPE>
 __device__ __forceinline__ RawRows<DT> load_rows(const void *p, int64_t ld, int64_t r0, int64_t c0, int live, int have)
 {
     const Spot at = spot<sizeof(typename Elem<DT>::T)>(p, ld, r0, c0);
     RawRows<DT> x;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x.row[i] = load_raw<DT, EIGHTS>(at.row(i), 0, i < live ? have : 0);
+    for (int i = 0; i < 4; ++i) x.row[i] = load_raw<DT, SHAPE != kAnyShape>(at.row(i), 0, i < live ? have : 0);
     return x;
 }
 
@@ -368,155 +379,163 @@ __device__ __forceinline__ void hold(RawRows<DT> &q)
     }
 }
 
-// One of dgate (WHAT 0), dup (1) and y (2), of four columns of row i.
-// Columns past the last are zeros (a scale that says NaN makes NaNs of their
-// zero codes).
-template <int DT, int ACT, bool CODED, bool EIGHTS, int WHAT, class In>
-__device__ __forceinline__ void grad4(const In &g, const In &u, const RawRows<DT> &d, int i, int h, int cnt, float v[4])
+template <bool CODED, int DT> struct GateIn { typedef CodedRows T; };
+template <int DT> struct GateIn<false, DT> { typedef RawRows<DT> T; };
+
+// Four columns of row i: dgate (PART 0) to v[0], or dup and y (PART 1) to v[0]
+// and v[1].  Columns past the last are zeros (a scale that says NaN makes NaNs of
+// their zero codes).
+template <int DT, int ACT, bool CODED, int SHAPE, int PART, class In>
+__device__ __forceinline__ void grad4(const In &g, const In &u, const RawRows<DT> &d, int i, int h, int cnt, float (&v)[PART + 1][4][8])
 {
     float gv[4], uv[4], dv[4];
     half_of(g, i, h, gv);
-    if (WHAT != 1) half_of(u, i, h, uv);
-    if (WHAT != 2) half_of(d, i, h, dv);
+    half_of(u, i, h, uv);
+    half_of(d, i, h, dv);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         float s, slope;
         act_slope<ACT, DT == kP32>(gv[k], s, slope);
-        v[k] = WHAT == 0 ? dv[k] * uv[k] * slope : WHAT == 1 ? dv[k] * s : s * uv[k];
-        if (CODED && !EIGHTS && 4 * h + k >= cnt) v[k] = 0.0f;
+        v[0][i][4 * h + k] = PART == 0 ? dv[k] * uv[k] * slope : dv[k] * s;
+        v[PART][i][4 * h + k] = PART == 0 ? v[0][i][4 * h + k] : s * uv[k];
+        if (CODED && SHAPE == kAnyShape && 4 * h + k >= cnt) v[0][i][4 * h + k] = v[PART][i][4 * h + k] = 0.0f;
     }
 }
 
-template <bool CODED, int DT> struct GateIn { typedef CodedRows T; };
-template <int DT> struct GateIn<false, DT> { typedef RawRows<DT> T; };
-
-// All outputs of one of the three matrices of a tile.
-template <int DT, int ACT, bool CODED, bool EIGHTS, int WHAT, class In>
-__device__ __forceinline__ void grad_part(const OPT_CONST GateGradArgs *a, TileLds<3> &lds, In &g, In &u, RawRows<DT> &d, int64_t r0, int64_t c0)
+// dgate or dup of a tile: as a matrix, and its codes by rows.
+template <int DT, int SHAPE>
+__device__ __forceinline__ void put_rows(const float (&v)[4][8], void *m, int64_t ld, const Codes &q, int64_t r0, int64_t c0, int64_t rows, int64_t cols)
 {
-    a = again(a);
-    void *const m = WHAT == 0 ? a->dgate : WHAT == 1 ? a->dup : nullptr;
-    const Codes q = WHAT == 0 ? copy(a->dgq) : WHAT == 1 ? copy(a->duq) : Codes{}, qt = copy(WHAT == 0 ? a->dgt : WHAT == 1 ? a->dut : a->yt);
-    if (!m && !q.codes && !qt.codes) return;
-    const int have = cols_of(a->cols, c0), live = rows_of(a->rows, r0);
-    hold(g);
-    hold(u);
-    hold(d);
-    float v[4][8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) grad4<DT, ACT, CODED, EIGHTS, WHAT>(g, u, d, i, h, i < live ? have : 0, v[i] + 4 * h);
+    const int have = cols_of<SHAPE>(cols, c0), live = rows_of<SHAPE>(rows, r0);
     if (m) {
-        const Spot at = spot<sizeof(typename Elem<DT>::T)>(m, WHAT == 0 ? a->lddg : a->lddu, r0, c0);
+        const Spot at = spot<sizeof(typename Elem<DT>::T)>(m, ld, r0, c0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) store8<DT, EIGHTS>(at.row(i), 0, i < live ? have : 0, v[i]);
-    }
-    if (qt.codes) {
-        float top[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top[k] = __builtin_elementwise_maximum(max_abs(v[0][k], v[1][k]), max_abs(v[2][k], v[3][k]));
-        add_tops(lds.top[WHAT], top);
+        for (int i = 0; i < 4; ++i) store8<DT, SHAPE != kAnyShape>(at.row(i), 0, i < live ? have : 0, v[i]);
     }
     if (q.codes) {
         const Spot at = spot<1>(q.codes, q.ld, r0, c0);
-        const bool padded = cols_of((a->cols + 15) & ~(int64_t)15, c0) > 0;
+        const bool padded = cols_of<SHAPE>((cols + 15) & ~(int64_t)15, c0) > 0;
         uint32_t mine = 0;             // lane i of a row keeps row i's scale: one store for the four
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t byte = block_scale(row16_max_u32(top8(v[i])));
-            const u2 code = codes8(v[i], byte);
+            uint32_t word;
+            const u2 code = code_block(v[i], row16_max_u32(top8(v[i])), word);
             if (i < live && padded) gst<u2>(at.row(i), code);
-            if ((threadIdx.x & 15) == i) mine = byte;
+            if ((threadIdx.x & 15) == i) mine = word;
         }
         if ((int)(threadIdx.x & 15) < live)
-            gst<uint8_t>(q.scales + (c0 / kCodeBlock) * q.lds + r0 + 4 * (threadIdx.x >> 4) + (threadIdx.x & 15), (uint8_t)mine);
+            gst<uint8_t>(q.scales + (c0 / kCodeBlock) * q.lds + r0 + 4 * (threadIdx.x >> 4) + (threadIdx.x & 15), (uint8_t)(mine >> 23));
     }
-    if (!qt.codes) return;
-    __syncthreads();
-    if (threadIdx.x < 128) set_scale(lds, WHAT, qt, r0, c0, a->cols);
-    __syncthreads();
-    const bool lost = lds.lost != 0;
-    const u4 x0 = *(const u4 *)(lds.top[WHAT] + 8 * (threadIdx.x & 15)), x1 = *(const u4 *)(lds.top[WHAT] + 8 * (threadIdx.x & 15) + 4);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) put_column(lds.tr[WHAT], k, k < 4 ? x0[k & 3] : x1[k & 3], lost, v[0][k], v[1][k], v[2][k], v[3][k]);
 }
 
-template <int DT, int ACT, bool CODED, bool EIGHTS>
+// The outputs of dgate, or of dup and y.
+template <int DT, int ACT, bool CODED, int SHAPE, int PART, class In>
+__device__ __forceinline__ void grad_part(const OPT_CONST GateGradArgs *a, TileLds<3> &lds, In &g, In &u, RawRows<DT> &d, int64_t r0, int64_t c0)
+{
+    a = again(a);
+    hold(g);
+    hold(u);
+    hold(d);
+    const int have = cols_of<SHAPE>(a->cols, c0), live = rows_of<SHAPE>(a->rows, r0);
+    float v[PART + 1][4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) grad4<DT, ACT, CODED, SHAPE, PART>(g, u, d, i, h, i < live ? have : 0, v);
+    const bool first = (PART ? a->dut.codes : a->dgt.codes) != nullptr, second = PART && a->yt.codes;
+    if (first) add_tops(lds.top[PART], v[0]);
+    if (second) add_tops(lds.top[2], v[PART]);
+    if (PART) put_rows<DT, SHAPE>(v[0], a->dup, a->lddu, copy(a->duq), r0, c0, a->rows, a->cols);
+    else put_rows<DT, SHAPE>(v[0], a->dgate, a->lddg, copy(a->dgq), r0, c0, a->rows, a->cols);
+    __syncthreads();
+    if (first) set_scales(lds, PART, PART ? copy(a->dut) : copy(a->dgt), r0, c0, a->cols);
+    if (second) set_scales(lds, 2, copy(a->yt), r0, c0, a->cols);
+    __syncthreads();
+    if (first) code_columns(lds, PART, v[0]);
+    if (second) code_columns(lds, 2, v[PART]);
+}
+
+template <int DT, int ACT, bool CODED, int SHAPE>
+__device__ __forceinline__ void grad_tile(const OPT_CONST GateGradArgs *a, TileLds<3> &lds, int64_t r0, int64_t c0)
+{
+    const int have = cols_of<SHAPE>(a->cols, c0), live = rows_of<SHAPE>(a->rows, r0);
+    typename GateIn<CODED, DT>::T g, u;
+    if constexpr (CODED) {
+        g = load_coded(copy(a->gq), r0, c0, have > 0 ? live : 0);
+        u = load_coded(copy(a->uq), r0, c0, have > 0 ? live : 0);
+    } else {
+        g = load_rows<DT, SHAPE>(a->gate, a->ldg, r0, c0, live, have);
+        u = load_rows<DT, SHAPE>(a->up, a->ldu, r0, c0, live, have);
+    }
+    RawRows<DT> d = load_rows<DT, SHAPE>(a->dy, a->lddy, r0, c0, live, have);
+    clear_tops(lds);
+    __syncthreads();
+    // dgate first, then dup and y from the inputs again: the three at once would take 96 registers for the values alone
+    grad_part<DT, ACT, CODED, SHAPE, 0>(a, lds, g, u, d, r0, c0);
+    grad_part<DT, ACT, CODED, SHAPE, 1>(a, lds, g, u, d, r0, c0);
+    __syncthreads();
+    a = again(a);
+    if (a->dgt.codes) put_tile<SHAPE>(lds, 0, copy(a->dgt), r0, c0, a->rows, a->cols);
+    if (a->dut.codes) put_tile<SHAPE>(lds, 1, copy(a->dut), r0, c0, a->rows, a->cols);
+    if (a->yt.codes) put_tile<SHAPE>(lds, 2, copy(a->yt), r0, c0, a->rows, a->cols);
+}
+
+template <int DT, int ACT, bool CODED, int SHAPE>
 __global__ __launch_bounds__(kTileThreads, DT == kP32 && !CODED ? 2 : 4) void gated_act_grad_kernel(GateGradArgs)
 {
     __shared__ TileLds<3> lds;
     const OPT_CONST GateGradArgs *a = kernargs<GateGradArgs>();
     for (int64_t r0 = (int64_t)blockIdx.y * 128; r0 < a->rows; r0 += (int64_t)gridDim.y * 128)
-    for (int64_t c0 = (int64_t)blockIdx.x * 128; c0 < a->cols; c0 += (int64_t)gridDim.x * 128) {
-        a = again(a);
-        const int have = cols_of(a->cols, c0), live = rows_of(a->rows, r0);
-        typename GateIn<CODED, DT>::T g, u;
-        if constexpr (CODED) {
-            g = load_coded(copy(a->gq), r0, c0, have > 0 ? live : 0);
-            u = load_coded(copy(a->uq), r0, c0, have > 0 ? live : 0);
-        } else {
-            g = load_rows<DT, EIGHTS>(a->gate, a->ldg, r0, c0, live, have);
-            u = load_rows<DT, EIGHTS>(a->up, a->ldu, r0, c0, live, have);
+        for (int64_t c0 = (int64_t)blockIdx.x * 128; c0 < a->cols; c0 += (int64_t)gridDim.x * 128) {
+            if (r0 != (int64_t)blockIdx.y * 128 || c0 != (int64_t)blockIdx.x * 128) __syncthreads();    // the LDS of the last tile is read
+            grad_tile<DT, ACT, CODED, SHAPE>(again(a), lds, r0, c0);
         }
-        RawRows<DT> d = load_rows<DT, EIGHTS>(a->dy, a->lddy, r0, c0, live, have);
-        clear_tops(lds);
-        __syncthreads();
-        // the three one after the other, each from the inputs: all at once would take 96 registers for the values alone
-        grad_part<DT, ACT, CODED, EIGHTS, 0>(a, lds, g, u, d, r0, c0);
-        grad_part<DT, ACT, CODED, EIGHTS, 1>(a, lds, g, u, d, r0, c0);
-        grad_part<DT, ACT, CODED, EIGHTS, 2>(a, lds, g, u, d, r0, c0);
-        __syncthreads();
-        a = again(a);
-        if (a->dgt.codes) put_tile(lds.tr[0], copy(a->dgt), r0, c0, a->rows, a->cols);
-        if (a->dut.codes) put_tile(lds.tr[1], copy(a->dut), r0, c0, a->rows, a->cols);
-        if (a->yt.codes) put_tile(lds.tr[2], copy(a->yt), r0, c0, a->rows, a->cols);
-    }
 }
 
 // Values of a coded matrix, and codes of its transpose.
-template <int DT, bool EIGHTS>
+template <int DT, int SHAPE>
+__device__ __forceinline__ void restore_tile(const OPT_CONST RestoreArgs *a, TileLds<1> &lds, int64_t r0, int64_t c0)
+{
+    const int have = cols_of<SHAPE>(a->cols, c0), live = rows_of<SHAPE>(a->rows, r0);
+    const CodedRows q = load_coded(copy(a->q), r0, c0, have > 0 ? live : 0);
+    const bool transposed = a->qt.codes;
+    if (transposed) {
+        clear_tops(lds);
+        __syncthreads();
+    }
+    float v[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        decode8(q.code[i], q.bytes >> (8 * i) & 255u, v[i]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (SHAPE == kAnyShape && k >= (i < live ? have : 0)) v[i][k] = 0.0f;
+    }
+    if (a->x) {
+        const Spot at = spot<sizeof(typename Elem<DT>::T)>(a->x, a->ldx, r0, c0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store8<DT, SHAPE != kAnyShape>(at.row(i), 0, i < live ? have : 0, v[i]);
+    }
+    if (!transposed) return;
+    add_tops(lds.top[0], v);
+    __syncthreads();
+    set_scales(lds, 0, copy(a->qt), r0, c0, a->cols);
+    __syncthreads();
+    code_columns(lds, 0, v);
+    __syncthreads();
+    put_tile<SHAPE>(lds, 0, copy(a->qt), r0, c0, a->rows, a->cols);
+}
+
+template <int DT, int SHAPE>
 __global__ __launch_bounds__(kTileThreads) void block_restore_kernel(RestoreArgs)
 {
     __shared__ TileLds<1> lds;
     const OPT_CONST RestoreArgs *a = kernargs<RestoreArgs>();
     for (int64_t r0 = (int64_t)blockIdx.y * 128; r0 < a->rows; r0 += (int64_t)gridDim.y * 128)
-    for (int64_t c0 = (int64_t)blockIdx.x * 128; c0 < a->cols; c0 += (int64_t)gridDim.x * 128) {
-        const int have = cols_of(a->cols, c0), live = rows_of(a->rows, r0);
-        const CodedRows q = load_coded(copy(a->q), r0, c0, have > 0 ? live : 0);
-        const bool transposed = a->qt.codes;
-        if (transposed) {
-            clear_tops(lds);
-            __syncthreads();
+        for (int64_t c0 = (int64_t)blockIdx.x * 128; c0 < a->cols; c0 += (int64_t)gridDim.x * 128) {
+            if (r0 != (int64_t)blockIdx.y * 128 || c0 != (int64_t)blockIdx.x * 128) __syncthreads();    // the LDS of the last tile is read
+            restore_tile<DT, SHAPE>(again(a), lds, r0, c0);
         }
-        float v[4][8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            decode8(q.code[i], q.bytes >> (8 * i) & 255u, v[i]);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (!EIGHTS && k >= (i < live ? have : 0)) v[i][k] = 0.0f;
-        }
-        if (a->x) {
-            const Spot at = spot<sizeof(typename Elem<DT>::T)>(a->x, a->ldx, r0, c0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) store8<DT, EIGHTS>(at.row(i), 0, i < live ? have : 0, v[i]);
-        }
-        if (!transposed) continue;
-        float top[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top[k] = __builtin_elementwise_maximum(max_abs(v[0][k], v[1][k]), max_abs(v[2][k], v[3][k]));
-        add_tops(lds.top[0], top);
-        __syncthreads();
-        if (threadIdx.x < 128) set_scale(lds, 0, copy(a->qt), r0, c0, a->cols);
-        __syncthreads();
-        const bool lost = lds.lost != 0;
-        const u4 x0 = *(const u4 *)(lds.top[0] + 8 * (threadIdx.x & 15)), x1 = *(const u4 *)(lds.top[0] + 8 * (threadIdx.x & 15) + 4);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) put_column(lds.tr[0], k, k < 4 ? x0[k & 3] : x1[k & 3], lost, v[0][k], v[1][k], v[2][k], v[3][k]);
-        __syncthreads();
-        put_tile(lds.tr[0], copy(a->qt), r0, c0, a->rows, a->cols);
-    }
 }
 
 // ---- launches --------------------------------------------------------------
@@ -540,14 +559,22 @@ static hipError_t launch_gate_t(const GateArgs &a, hipStream_t st)
     return hipGetLastError();
 }
 
-template <int DT, int ACT, bool CODED, bool EIGHTS>
+static int shape_of(int64_t rows, int64_t cols) { return rows % 128 == 0 && cols % 128 == 0 ? kFull : cols % 8 == 0 ? kEights : kAnyShape; }
+
+template <int DT, int ACT, bool CODED>
 static hipError_t launch_gate_grad_t(const GateGradArgs &a, hipStream_t st)
 {
-    if (a.dgt.codes || a.dut.codes || a.yt.codes) {
-        hipLaunchKernelGGL((gated_act_grad_kernel<DT, ACT, CODED, EIGHTS>), tiles_of(a.rows, a.cols), dim3(kTileThreads), 0, st, a);
-    } else {
-        const int64_t tiles = ((a.cols + 127) / 128) * ((a.rows + kGateRows - 1) / kGateRows);
-        hipLaunchKernelGGL((gated_act_grad_rows_kernel<DT, ACT, CODED, EIGHTS>), dim3(grid_of(tiles)), dim3(256), 0, st, a);
+    if (!a.dgt.codes && !a.dut.codes && !a.yt.codes) {
+        const unsigned grid = grid_of(((a.cols + 127) / 128) * ((a.rows + kGateRows - 1) / kGateRows));
+        if (a.cols % 8 == 0) hipLaunchKernelGGL((gated_act_grad_rows_kernel<DT, ACT, CODED, true>), dim3(grid), dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((gated_act_grad_rows_kernel<DT, ACT, CODED, false>), dim3(grid), dim3(256), 0, st, a);
+        return hipGetLastError();
+    }
+    const dim3 grid = tiles_of(a.rows, a.cols);
+    switch (shape_of(a.rows, a.cols)) {
+    case kFull: hipLaunchKernelGGL((gated_act_grad_kernel<DT, ACT, CODED, kFull>), grid, dim3(kTileThreads), 0, st, a); break;
+    case kEights: hipLaunchKernelGGL((gated_act_grad_kernel<DT, ACT, CODED, kEights>), grid, dim3(kTileThreads), 0, st, a); break;
+    default: hipLaunchKernelGGL((gated_act_grad_kernel<DT, ACT, CODED, kAnyShape>), grid, dim3(kTileThreads), 0, st, a);
     }
     return hipGetLastError();
 }
@@ -555,17 +582,18 @@ static hipError_t launch_gate_grad_t(const GateGradArgs &a, hipStream_t st)
 template <int DT, int ACT>
 static hipError_t launch_gate_grad_a(const GateGradArgs &a, hipStream_t st)
 {
-    const bool eights = a.cols % 8 == 0;
-    if (a.gate) return eights ? launch_gate_grad_t<DT, ACT, false, true>(a, st) : launch_gate_grad_t<DT, ACT, false, false>(a, st);
-    return eights ? launch_gate_grad_t<DT, ACT, true, true>(a, st) : launch_gate_grad_t<DT, ACT, true, false>(a, st);
+    return a.gate ? launch_gate_grad_t<DT, ACT, false>(a, st) : launch_gate_grad_t<DT, ACT, true>(a, st);
 }
 
 template <int DT>
 static hipError_t launch_restore_t(const RestoreArgs &a, hipStream_t st)
 {
     const dim3 grid = tiles_of(a.rows, a.cols);
-    if (a.cols % 8 == 0) hipLaunchKernelGGL((block_restore_kernel<DT, true>), grid, dim3(kTileThreads), 0, st, a);
-    else hipLaunchKernelGGL((block_restore_kernel<DT, false>), grid, dim3(kTileThreads), 0, st, a);
+    switch (shape_of(a.rows, a.cols)) {
+    case kFull: hipLaunchKernelGGL((block_restore_kernel<DT, kFull>), grid, dim3(kTileThreads), 0, st, a); break;
+    case kEights: hipLaunchKernelGGL((block_restore_kernel<DT, kEights>), grid, dim3(kTileThreads), 0, st, a); break;
+    default: hipLaunchKernelGGL((block_restore_kernel<DT, kAnyShape>), grid, dim3(kTileThreads), 0, st, a);
+    }
     return hipGetLastError();
 }
 

@@ -164,11 +164,11 @@ __global__ __launch_bounds__(kHeadThreads) void head_norm_kernel(HeadArgs a, int
             }
             store8<DT, MODE == kHalves>(s.y, token * s.yt + head * s.yh + c, n, y);
             if (s.q.codes) {
-                const uint32_t byte = block_scale(block_max_u32<L>(top8(x)));
-                const u2 code = codes8(x, byte);
+                uint32_t word;
+                const u2 code = code_block(x, block_max_u32<L>(top8(x)), word);
                 const int64_t line = token * s.heads + head;
                 if (live && c < ((t.dim + 15) & ~15)) gst<u2>(s.q.codes + line * s.q.ld + c, code);
-                if (n > 0 && (lane & 15) == 0) gst<uint8_t>(s.q.scales + (c / kCodeBlock) * s.q.lds + line, (uint8_t)byte);
+                if (n > 0 && (lane & 15) == 0) gst<uint8_t>(s.q.scales + (c / kCodeBlock) * s.q.lds + line, (uint8_t)(word >> 23));
             }
         }
     }

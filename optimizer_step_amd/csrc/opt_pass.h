@@ -402,16 +402,40 @@ __device__ __forceinline__ u2 encode8(const float v[8], uint32_t byte)
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, uint32_t x)
 {
     typedef short pair __attribute__((ext_vector_type(2)));
-    pair w = {0, 0};
+    pair w;
+    w = __builtin_nondeterministic_value(w);    // each half is written: no register is cleared first
     w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, bitsf(x), false);
     w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, bitsf(x), true);
     return __builtin_bit_cast(uint32_t, w);
 }
 
-__device__ __forceinline__ u2 codes8(const float v[8], uint32_t byte)
+// The scale of a block whose largest magnitude has the bits `a`, as that word:
+// block_scale(a) << 23 in three instructions, for a finite block (adding
+// 0x1FFFFF carries into the exponent where the significand passes 1.75).
+__device__ __forceinline__ uint32_t scale_word(uint32_t a)
 {
-    const u2 w = {codes4(v[0], v[1], v[2], v[3], byte << 23), codes4(v[4], v[5], v[6], v[7], byte << 23)};
-    return byte == 255u ? (u2){0u, 0u} : w;
+    return __builtin_elementwise_sub_sat((a + 0x1FFFFFu) & 0x7F800000u, 8u << 23);
+}
+
+constexpr uint32_t kLostWord = 255u << 23;     // of a block that holds a NaN or an infinity
+
+__device__ __forceinline__ u2 codes8(const float v[8], uint32_t word)
+{
+    return (u2){codes4(v[0], v[1], v[2], v[3], word), codes4(v[4], v[5], v[6], v[7], word)};
+}
+
+// Codes of eight values of a block whose largest magnitude has the bits `a`;
+// word becomes its scale's.  Every lane of the wave calls it: lost blocks, whose
+// codes are zeros, are looked at only where the wave has one.
+__device__ __forceinline__ u2 code_block(const float v[8], uint32_t a, uint32_t &word)
+{
+    word = scale_word(a);
+    u2 code = codes8(v, word);
+    if (__any(a >= 0x7F800000u) && a >= 0x7F800000u) {
+        word = kLostWord;
+        code = (u2){0u, 0u};
+    }
+    return code;
 }
 
 // Eight values of a block-coded row, from its codes and their scale's byte:
@@ -430,8 +454,9 @@ __device__ __forceinline__ void decode8(u2 code, uint32_t byte, float v[8])
     }
 }
 
-// Bits of the largest magnitude of eight values, a NaN's if one is NaN: the
-// maximum that propagates NaNs takes three operands and their magnitudes at once.
+// Bits of the largest magnitude of eight values; 0x7F800000 or more if one is
+// infinite or NaN (of either sign): the maximum that propagates NaNs takes three
+// operands and their magnitudes at once.
 __device__ __forceinline__ float max_abs(float a, float b)
 {
     return __builtin_elementwise_maximum(__builtin_fabsf(a), __builtin_fabsf(b));
@@ -442,7 +467,7 @@ __device__ __forceinline__ uint32_t top8(const float v[8])
     float m = max_abs(v[0], v[1]);
 #pragma unroll
     for (int i = 2; i < 8; i += 2) m = __builtin_elementwise_maximum(m, max_abs(v[i], v[i + 1]));
-    return fbits(m) & 0x7FFFFFFFu;
+    return fbits(m);
 }
 
 }  // namespace optstep
