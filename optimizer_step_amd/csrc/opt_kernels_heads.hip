@@ -2,33 +2,56 @@
 // rotation by position in the same pass, and its backward pass.
 //
 // Forward, for each head x of dim elements:  r = fl(1/sqrt(mean(x^2) + eps)),
-// n = (x r) w, and the first rot elements turn in pairs (a, b) by the angle
-// whose cosine c and sine s the position's row of the table holds:
-// (a c - b s, b c + a s).  Backward: dn is dy turned the other way, g = dn w,
-// k = mean(g x), dx = r (g - x r^2 k), dw = sum over tokens and heads of
-// dn (x r).
+// n = x r w, and the first rot elements turn in pairs (a, b) by the angle whose
+// cosine c and sine s the position's row of the table holds: (a c - b s,
+// b c + a s).  Backward: dn is dy turned the other way, g = dn w, k = r^2
+// mean(g x), dx = r (g - x k), dw = sum over tokens and heads of dn (x r).
 //
 // A head stays in the registers of L lanes, eight consecutive elements each; a
-// wave holds 64/L heads (a unit) of one token and one of the two sets, and takes
-// `per` units in turn, so that the token's angles are read once for them.
+// wave holds 64/L heads (a unit) of one token.  What an element takes of itself
+// and of its pair's other half, A = w c and B = w' (+-)s with the partner's
+// weight w', is the same for all of a token's heads and formed once for them:
+// y = (x r) A + (x' r) B.
+//
+// Bound by HBM and by the latency of a wave's chain (position, table's row and
+// elements, sums, root).  8192 tokens of 32 + 8 heads of 128, bf16: forward with
+// codes 42 us (215 MB, 5.1 TB/s), without 36; backward from codes 48 us and 4 for
+// the sums of both weights' gradients (214 MB, 4.1 TB/s; the vector units are busy
+// half the time).  Stores carry the non-temporal hint (51.7 us forward without);
+// so do the loads where no codes are written (43.8 -> 37.9 us; with codes 43.9
+// -> 45.7) and the backward pass's (53.1 -> 51.1).
 #include "opt_pass.h"
 
 namespace optstep {
 
-constexpr int kHeadThreads = 256;
-
 // How a pair's other element is found.  kHalves: pairs (i, i + rot/2) with
-// rot/2 and dim multiples of eight, so that the partners of a lane's eight are
-// eight consecutive elements too.  kAny: everything else, element by element.
-enum { kHalves = 0, kAny = 1 };
+// rot/2 and dim multiples of eight (or no pairs): a lane's partners are another
+// lane's eight.  kWhole: the same where the head fills its lanes (dim = 8 L), so
+// that no lane's loads are masked.  kNear: pairs (2 i, 2 i + 1), dim a multiple
+// of eight: a lane's own.  kAny: what is left, element by element.
+enum { kWhole = 0, kHalves = 1, kNear = 2, kAny = 3 };
+constexpr bool by_halves(int mode) { return mode <= kHalves; }
 
-// A token's row of the table; 0 if its position has none.
+// A token's row of the table; null if its position has none.
 __device__ __forceinline__ const float *table_row(const HeadTurn &t, int64_t token)
 {
     int64_t p = token;
-    if (t.positions) p = t.wide_positions ? gld<int64_t>((const int64_t *)t.positions + token) : (int64_t)gld<int32_t>((const int32_t *)t.positions + token);
+    if (t.positions)       // the token is the wave's: a scalar load
+        p = t.wide_positions ? ((const OPT_CONST int64_t *)t.positions)[token] : (int64_t)((const OPT_CONST int32_t *)t.positions)[token];
     if (p < 0 || p >= t.table_rows) return nullptr;
     return t.table + p * t.ldt;
+}
+
+// Where an element of the first rot has its partner, whether it is a pair's
+// first, and which pair that is.
+struct Pair { int partner, index; bool first; };
+
+template <int MODE>
+__device__ __forceinline__ Pair pair_of(const HeadTurn &t, int e)
+{
+    const int h = t.rot / 2;
+    if (MODE == kNear || (MODE == kAny && t.neighbours)) return Pair{e ^ 1, e >> 1, !(e & 1)};
+    return Pair{e < h ? e + h : e - h, e < h ? e : e - h, e < h};
 }
 
 // cos and sin of the eight elements from c on, the sine with the sign of what
@@ -36,72 +59,94 @@ __device__ __forceinline__ const float *table_row(const HeadTurn &t, int64_t tok
 template <int MODE, bool BACK>
 __device__ __forceinline__ void angles(const HeadTurn &t, const float *row, int c, float cs[8], float sn[8])
 {
-    const int h = t.rot / 2;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         cs[i] = 1.0f;
         sn[i] = 0.0f;
     }
-    if (!row) return;
-    if (MODE == kHalves) {
-        if (c < t.rot) {
-            const bool first = c < h;
-            const float *p = row + (first ? c : c - h);
-            load8<kP32>(p, 0, 8, cs);
-            load8<kP32>(p + h, 0, 8, sn);
+    if (!row || c >= t.rot) return;
+    if (by_halves(MODE)) {
+        const Pair p = pair_of<MODE>(t, c);
+        load8<kP32, true>(row + p.index, 0, 8, cs);
+        load8<kP32, true>(row + t.rot / 2 + p.index, 0, 8, sn);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sn[i] = first != BACK ? -sn[i] : sn[i];
-        }
+        for (int i = 0; i < 8; ++i) sn[i] = p.first != BACK ? -sn[i] : sn[i];
         return;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int e = c + i;
-        if (e < t.rot) {
-            const bool first = t.neighbours ? !(e & 1) : e < h;
-            const int j = t.neighbours ? e >> 1 : first ? e : e - h;
-            cs[i] = gld<float>(row + j);
-            sn[i] = gld<float>(row + h + j);
-            sn[i] = first != BACK ? -sn[i] : sn[i];
-        }
+        if (c + i >= t.rot) break;
+        const Pair p = pair_of<MODE>(t, c + i);
+        cs[i] = gld<float>(row + p.index);
+        sn[i] = gld<float>(row + t.rot / 2 + p.index);
+        sn[i] = p.first != BACK ? -sn[i] : sn[i];
     }
 }
 
-// The partners of the eight elements from c on, out of a head's row at p + at
-// (elements that do not turn are their own).
-template <int DT, int MODE>
-__device__ __forceinline__ void partners(int dt, const HeadTurn &t, const void *p, int64_t at, int c, int cnt, const float own[8], float v[8])
+__device__ __forceinline__ float load_any(int dt, const void *p, int64_t j)
 {
-    const int h = t.rot / 2;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = own[i];
-    if (MODE == kHalves) {
-        if (c < t.rot && cnt > 0) {
-            const int64_t j = at + (c < h ? c + h : c - h);
-            if (DT >= 0) load8<DT < 0 ? 0 : DT, true>(p, j, 8, v);
-            else load8_any<true>(dt, p, j, 8, v);
-        }
-        return;
-    }
-    if (t.neighbours) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = own[i ^ 1];
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int e = c + i;
-        if (e < t.rot && i < cnt) {
-            const int64_t j = at + (e < h ? e + h : e - h);
-            const int d = DT >= 0 ? DT : dt;
-            if (d == kP32) v[i] = gld<float>((const float *)p + j);
-            else {
-                const uint32_t b = gld<uint16_t>((const uint16_t *)p + j);
-                v[i] = d == kPBF16 ? bf16_lo(b) : f16_lo(b);
-            }
-        }
-    }
+    if (dt == kP32) return gld<float>((const float *)p + j);
+    const uint32_t b = gld<uint16_t>((const uint16_t *)p + j);
+    return dt == kPBF16 ? bf16_lo(b) : f16_lo(b);
 }
+
+// The weights of the eight elements from c on, and (PARTNERS) of their partners.
+template <int MODE, bool PARTNERS>
+__device__ __forceinline__ void weights(const HeadTurn &t, const void *w, int c, int cnt, float v[8], float vp[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = vp[i] = 1.0f;
+    if (!w) return;
+    load8_any<MODE != kAny>(t.w_dtype, w, c, cnt, v);
+    if (!PARTNERS || c >= t.rot) return;
+    if (by_halves(MODE)) {
+        load8_any<true>(t.w_dtype, w, pair_of<MODE>(t, c).partner, cnt, vp);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c + i < t.rot) vp[i] = load_any(t.w_dtype, w, pair_of<MODE>(t, c + i).partner);
+}
+
+// The partners of a lane's eight elements of a head whose row begins at p.  Every
+// lane of the wave calls it.
+template <int DT, int L, int MODE>
+__device__ __forceinline__ void partners(const HeadTurn &t, const Raw<DT> &raw, const void *p, int c, int cnt, float v[8])
+{
+    if (by_halves(MODE)) {
+        // the lane h/8 up or down the head; what it holds, as stored
+        const int lane = threadIdx.x & 63, d = t.rot / 16;
+        const int from = 4 * (c >= t.rot ? lane : c < t.rot / 2 ? lane + d : lane - d);
+        Raw<DT> o;
+#pragma unroll
+        for (int j = 0; j < (DT == kP32 ? 2 : 1); ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o.v[j][i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)raw.v[j][i]);
+        unpack_raw<DT>(o, v);
+        return;
+    }
+    unpack_raw<DT>(raw, v);
+    if (MODE == kNear || t.neighbours) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const float x = v[i];
+            v[i] = v[i + 1];
+            v[i + 1] = x;
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < cnt && c + i < t.rot) v[i] = load_any(DT, p, pair_of<MODE>(t, c + i).partner);
+}
+
+__device__ __forceinline__ HeadTurn turn_of(const OPT_CONST HeadTurn &t)
+{
+    return HeadTurn{t.tokens, t.table_rows, t.ldt, t.table, t.positions, t.dim, t.rot, t.wide_positions, t.neighbours, t.w_dtype, t.eps, t.inv_dim};
+}
+
+// A forward launch's arguments.
+struct HeadLaunch { HeadArgs a; int per; };
 
 // Largest over the lanes that share one 128-element block.
 template <int L>
@@ -113,141 +158,272 @@ __device__ __forceinline__ uint32_t block_max_u32(uint32_t v)
     return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true));
 }
 
-template <int L>
-__device__ __forceinline__ double sum_squares(const float x[8])
+__device__ __forceinline__ float root_of(double ss, const HeadTurn &t) { return (float)inverse_root(__builtin_fma(ss, t.inv_dim, t.eps)); }
+
+// Loads of a unit's lanes: a head past the last reads the last one's elements
+// (kWhole) or none.
+template <int DT, int MODE, bool NT>
+__device__ __forceinline__ Raw<DT> load_head(const char *p, int c, int cnt)
 {
-    double ss = 0.0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = __builtin_fma((double)x[i], (double)x[i], ss);
-    return lanes_sum<L>(ss);
+    if (MODE == kWhole) return load_raw<DT, true, NT>(p, c, 8);
+    return load_raw<DT, MODE != kAny, NT>(p, c, cnt);
 }
 
-template <int DT, int L, int MODE>
-__global__ __launch_bounds__(kHeadThreads) void head_norm_kernel(HeadArgs a, int per)
+// Ends when the loads of x have arrived.  A wave asks for all its heads at once
+// and waits here once: the hardware counts loads and stores together, so that a
+// load waited for after a store waits for the store too.
+template <int DT, int N>
+__device__ __forceinline__ void arrived(Raw<DT> (&x)[N])
 {
-    constexpr int S = 64 / L;
-    const HeadTurn &t = a.t;
-    const int64_t u0 = (a.s[0].heads + S - 1) / S, units = u0 + (a.s[1].heads + S - 1) / S;
-    const int64_t chunks = (units + per - 1) / per;
-    const int lane = threadIdx.x % L, c = 8 * lane;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        asm volatile("" : "+v"(x[i].v[0]));
+        if (DT == kP32) asm volatile("" : "+v"(x[i].v[DT == kP32]));
+    }
+}
+
+constexpr int kHeadThreads = 256;
+
+// Units a wave takes at most: their elements are in its registers at once (at
+// 8192 tokens of 32 + 8 heads of 128, ten units a token: 3 measured 48.8 us, 4
+// 43.1, 5 42.1, 6 43.1).
+template <int DT> constexpr int head_most() { return DT == kP32 ? 3 : 5; }
+
+// A wave takes `per` units of a token, of the queries and then of the keys, all
+// of whose elements it asks for first.
+template <int DT, int L, int MODE, bool CODES>
+__global__ __launch_bounds__(kHeadThreads) void head_norm_kernel(HeadArgs, int)
+{
+    constexpr int S = 64 / L, kSize = sizeof(typename Elem<DT>::T), kMost = head_most<DT>();
+    const OPT_CONST HeadLaunch *k = kernargs<HeadLaunch>();
+    const HeadTurn t = turn_of(k->a.t);
+    const int per = k->per, lane = threadIdx.x % L, c = 8 * lane, slot = (threadIdx.x & 63) / L;
     const int cnt = left8(c, t.dim);
-    const int64_t waves = t.tokens * chunks, step = (int64_t)gridDim.x * (kHeadThreads / 64);
-    for (int64_t w = (int64_t)blockIdx.x * (kHeadThreads / 64) + threadIdx.x / 64; w < waves; w += step) {
-        const int64_t token = w / chunks, first = (w % chunks) * per;
+    const int headsq = (int)k->a.s[0].heads, headsk = (int)k->a.s[1].heads;
+    const int unitsq = (headsq + S - 1) / S, units = unitsq + (headsk + S - 1) / S, parts = (units + per - 1) / per;
+    const int64_t waves = t.tokens * parts, step = (int64_t)gridDim.x * (kHeadThreads / 64);
+    for (int64_t w = (int64_t)blockIdx.x * (kHeadThreads / 64) + wave_id(); w < waves; w += step) {
+        const int64_t token = parts == 1 ? w : w < (int64_t)1 << 31 ? (uint32_t)w / (uint32_t)parts : w / parts;
+        const int first = (int)(w - token * parts) * per, n = units - first < per ? units - first : per;
+        // past the last head of a set: kWhole does that head's work again, to the same places
+        auto head_of = [&](int u, bool keys) {
+            const int head = (u - (keys ? unitsq : 0)) * S + slot, heads = keys ? headsk : headsq;
+            return MODE == kWhole && head >= heads ? heads - 1 : head;
+        };
+        Raw<DT> raw[kMost];
+#pragma unroll
+        for (int j = 0; j < kMost; ++j)
+            if (j < n) {
+                const bool keys = first + j >= unitsq;
+                const OPT_CONST HeadSet *h = k->a.s + keys;
+                const int head = head_of(first + j, keys);
+                const char *x = (const char *)h->x + token * h->xt * kSize + head * (h->xh * kSize);
+                raw[j] = load_head<DT, MODE, !CODES>(x, c, head < (keys ? headsk : headsq) ? cnt : 0);
+            }
         const float *row = t.rot ? table_row(t, token) : nullptr;
         const bool lost = t.rot && !row;            // a position the table does not hold: NaN
-        float cs[8], sn[8];
+        float A[2][8], B[2][8], cs[8], sn[8];
         angles<MODE, false>(t, row, c, cs, sn);
-        for (int64_t u = first; u < first + per && u < units; ++u) {
-            const int set = u >= u0;
-            const HeadSet &s = a.s[set];
-            const int64_t head = (u - (set ? u0 : 0)) * S + (threadIdx.x & 63) / L;
-            const bool live = head < s.heads;
-            const int n = live ? cnt : 0;
-            float x[8], xp[8], wt[8], wp[8], y[8];
-            const int64_t at = token * s.xt + head * s.xh;
-            load8<DT, MODE == kHalves>(s.x, at + c, n, x);
-            partners<DT, MODE>(0, t, s.x, at, c, n, x, xp);
-            if (s.w) {
-                load8_any<MODE == kHalves>(t.w_dtype, s.w, c, cnt, wt);
-                partners<-1, MODE>(t.w_dtype, t, s.w, 0, c, cnt, wt, wp);
-            } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) wt[i] = wp[i] = 1.0f;
-            }
-            float r = (float)inverse_root(__builtin_fma(sum_squares<L>(x), t.inv_dim, t.eps));
-            if (lost) r = bitsf(0x7FC00000u);
+        for (int set = 0; set < 2; ++set) {
+            if (set ? first + n <= unitsq : first >= unitsq) continue;
+            weights<MODE, true>(t, k->a.s[set].w, c, cnt, A[set], B[set]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float v = (x[i] * r) * wt[i], vp = (xp[i] * r) * wp[i];
-                y[i] = c + i < t.rot ? v * cs[i] + vp * sn[i] : v;
+                A[set][i] *= cs[i];
+                B[set][i] *= sn[i];
             }
-            store8<DT, MODE == kHalves>(s.y, token * s.yt + head * s.yh + c, n, y);
-            if (s.q.codes) {
+        }
+        arrived(raw);
+        const OPT_CONST HeadSet *h = k->a.s;
+#pragma unroll
+        for (int j = 0; j < kMost; ++j) {
+            if (j >= n) break;
+            const bool keys = first + j >= unitsq;
+            h = again(k)->a.s + keys;
+            if (first + j == unitsq || (j == 0 && keys))
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    A[0][i] = A[1][i];
+                    B[0][i] = B[1][i];
+                }
+            const int head = head_of(first + j, keys), heads = keys ? headsk : headsq;
+            const bool live = head < heads;
+            const int have = MODE == kWhole ? 8 : live ? cnt : 0;
+            float v[8], vp[8], o[8];
+            unpack_raw<DT>(raw[j], v);
+            partners<DT, L, MODE>(t, raw[j], (const char *)h->x + token * h->xt * kSize + head * (h->xh * kSize), c, have, vp);
+            double ss = 0.0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = __builtin_fma((double)v[i], (double)v[i], ss);
+            float r = root_of(lanes_sum<L>(ss), t);
+            if (lost) r = bitsf(0x7FC00000u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = __builtin_fmaf(vp[i] * r, B[0][i], (v[i] * r) * A[0][i]);
+            store8<DT, MODE != kAny, true>((char *)h->y + token * h->yt * kSize + head * (h->yh * kSize), c, have, o);
+            if (CODES && h->q.codes) {
+                const Codes q = copy(h->q);
                 uint32_t word;
-                const u2 code = code_block(x, block_max_u32<L>(top8(x)), word);
-                const int64_t line = token * s.heads + head;
-                if (live && c < ((t.dim + 15) & ~15)) gst<u2>(s.q.codes + line * s.q.ld + c, code);
-                if (n > 0 && (lane & 15) == 0) gst<uint8_t>(s.q.scales + (c / kCodeBlock) * s.q.lds + line, (uint8_t)(word >> 23));
+                const u2 code = code_block(v, block_max_u32<L>(top8(v)), word);
+                const int64_t line = token * heads + head;
+                if (MODE == kWhole || (live && c < ((t.dim + 15) & ~15))) sst<u2>(q.codes + line * q.ld + c, code);
+                if (MODE == kWhole || (have > 0 && (lane & 15) == 0)) gst<uint8_t>(q.scales + (c / kCodeBlock) * q.lds + line, (uint8_t)(word >> 23));
             }
         }
     }
 }
 
-template <int DT, int L, int MODE, bool CODED>
-__global__ __launch_bounds__(kHeadThreads) void head_norm_grad_kernel(HeadGradArgs a)
+// The backward pass: a wave takes tokens in turn and keeps its sums of both
+// weights' gradients in registers.
+constexpr int kHeadGradThreads = 256;
+constexpr int64_t kHeadGradGroups = 1024;    // four waves a SIMD; 512 measured 72 us against 55 at the sizes above
+
+// A lane's inputs of one head, as they are stored.
+template <int DT, bool CODED> struct HeadIn { Raw<DT> dy, x; };
+template <int DT> struct HeadIn<DT, true> { Raw<DT> dy; u2 x; uint32_t byte; };
+
+template <int DT, int N>
+__device__ __forceinline__ void arrived(HeadIn<DT, false> (&x)[N])
 {
-    constexpr int S = 64 / L;
-    __shared__ float comb[4][2][L * 8];
-    const HeadTurn &t = a.t;
-    const int lane = threadIdx.x % L, c = 8 * lane;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        asm volatile("" : "+v"(x[i].dy.v[0]), "+v"(x[i].x.v[0]));
+        if (DT == kP32) asm volatile("" : "+v"(x[i].dy.v[DT == kP32]), "+v"(x[i].x.v[DT == kP32]));
+    }
+}
+
+template <int DT, int N>
+__device__ __forceinline__ void arrived(HeadIn<DT, true> (&x)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        asm volatile("" : "+v"(x[i].dy.v[0]), "+v"(x[i].x), "+v"(x[i].byte));
+        if (DT == kP32) asm volatile("" : "+v"(x[i].dy.v[DT == kP32]));
+    }
+}
+
+template <int DT, bool CODED> constexpr int head_grad_most() { return DT == kP32 ? 2 : 4; }
+
+template <int DT, int L, int MODE, bool CODED>
+__global__ __launch_bounds__(kHeadGradThreads) void head_norm_grad_kernel(HeadGradArgs)
+{
+    constexpr int kWaves = kHeadGradThreads / 64, S = 64 / L, kSize = sizeof(typename Elem<DT>::T), kMost = head_grad_most<DT, CODED>();
+    __shared__ float comb[kWaves][2][L * 8];
+    const OPT_CONST HeadGradArgs *k = kernargs<HeadGradArgs>();
+    const HeadTurn t = turn_of(k->t);
+    const int lane = threadIdx.x % L, c = 8 * lane, slot = (threadIdx.x & 63) / L;
     const int cnt = left8(c, t.dim);
     float dw[2][8] = {};
-    const int64_t waves = t.tokens, step = (int64_t)gridDim.x * (kHeadThreads / 64);
-    for (int64_t token = (int64_t)blockIdx.x * (kHeadThreads / 64) + threadIdx.x / 64; token < waves; token += step) {
-        const float *row = t.rot ? table_row(t, token) : nullptr;
-        const bool lost = t.rot && !row;
+    const int64_t step = (int64_t)gridDim.x * kWaves;
+    const int headsq = (int)k->s[0].heads, headsk = (int)k->s[1].heads;
+    const int unitsq = (headsq + S - 1) / S, units = unitsq + (headsk + S - 1) / S;
+    const int parts = (units + kMost - 1) / kMost, per = (units + parts - 1) / parts;
+    float wq[8], wk[8], none[8];
+    weights<MODE, false>(t, k->s[0].w, c, cnt, wq, none);
+    weights<MODE, false>(t, k->s[1].w, c, cnt, wk, none);
+    for (int64_t token = (int64_t)blockIdx.x * kWaves + wave_id(); token < t.tokens; token += step) {
         float cs[8], sn[8];
-        angles<MODE, true>(t, row, c, cs, sn);
+        bool lost = false;
+#pragma unroll 1
+        for (int first = 0; first < units; first += per) {
+            const int n = units - first < per ? units - first : per;
+            // past the last head of a set: kWhole does that head's work again, to the same places
+            auto head_of = [&](int u, bool keys) {
+                const int head = (u - (keys ? unitsq : 0)) * S + slot, heads = keys ? headsk : headsq;
+                return MODE == kWhole && head >= heads ? heads - 1 : head;
+            };
+            HeadIn<DT, CODED> in[kMost];
 #pragma unroll
-        for (int set = 0; set < 2; ++set)
-        for (int64_t head0 = 0; head0 < a.s[set].heads; head0 += S) {
-            const HeadGradSet &s = a.s[set];
-            const int64_t head = head0 + (threadIdx.x & 63) / L;
-            const bool live = head < s.heads;
-            const int n = live ? cnt : 0;
-            float x[8], d[8], dp[8], wt[8], dx[8], g[8];
-            const int64_t dat = token * s.dyt + head * s.dyh, line = token * s.heads + head;
-            load8<DT, MODE == kHalves>(s.dy, dat + c, n, d);
-            partners<DT, MODE>(0, t, s.dy, dat, c, n, d, dp);
-            if (CODED) {
-                u2 code = {0u, 0u};
-                uint32_t byte = 127u;
-                if (n > 0) {
-                    code = gld<u2>(s.q.codes + line * s.q.ld + c);
-                    byte = gld<uint8_t>(s.q.scales + (c / kCodeBlock) * s.q.lds + line);
+            for (int j = 0; j < kMost; ++j)
+                if (j < n) {
+                    const bool keys = first + j >= unitsq;
+                    const OPT_CONST HeadGradSet *h = k->s + keys;
+                    const int head = head_of(first + j, keys), heads = keys ? headsk : headsq, have = head < heads ? cnt : 0;
+                    in[j].dy = load_head<DT, MODE, true>((const char *)h->dy + token * h->dyt * kSize + head * (h->dyh * kSize), c, have);
+                    if constexpr (CODED) {
+                        const Codes q = copy(h->q);
+                        const int64_t line = token * heads + head;
+                        in[j].x = (u2){0u, 0u};
+                        in[j].byte = 0;
+                        if (MODE == kWhole || have > 0) {
+                            in[j].x = gld<u2>(q.codes + line * q.ld + c);
+                            in[j].byte = gld<uint8_t>(q.scales + (c / kCodeBlock) * q.lds + line);
+                        }
+                    } else {
+                        in[j].x = load_head<DT, MODE, true>((const char *)h->x + token * h->xt * kSize + head * (h->xh * kSize), c, have);
+                    }
                 }
-                decode8(code, byte, x);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = i < n ? x[i] : 0.0f;
-            } else {
-                load8<DT, MODE == kHalves>(s.x, token * s.xt + head * s.xh + c, n, x);
+            if (first == 0) {
+                const float *row = t.rot ? table_row(t, token) : nullptr;
+                lost = t.rot && !row;
+                angles<MODE, true>(t, row, c, cs, sn);
             }
-            if (s.w) load8_any<MODE == kHalves>(t.w_dtype, s.w, c, cnt, wt);
-            double sg = 0.0;
+            arrived(in);
+            const OPT_CONST HeadGradSet *h = k->s;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (c + i < t.rot) d[i] = d[i] * cs[i] + dp[i] * sn[i];
-                g[i] = s.w ? d[i] * wt[i] : d[i];
-                sg = __builtin_fma((double)g[i], (double)x[i], sg);
-            }
-            float r = (float)inverse_root(__builtin_fma(sum_squares<L>(x), t.inv_dim, t.eps));
-            if (lost) r = bitsf(0x7FC00000u);
-            const float k = (float)((double)r * (double)r * (lanes_sum<L>(sg) * t.inv_dim));
+            for (int j = 0; j < kMost; ++j) {
+                if (j >= n) break;
+                const bool keys = first + j >= unitsq;
+                h = again(k)->s + keys;
+                const int head = head_of(first + j, keys);
+                const bool live = (first + j - (keys ? unitsq : 0)) * S + slot < (keys ? headsk : headsq);
+                const int have = MODE == kWhole ? 8 : live ? cnt : 0;
+                float v[8], d[8], dp[8], g[8], o[8];
+                unpack_raw<DT>(in[j].dy, d);
+                partners<DT, L, MODE>(t, in[j].dy, (const char *)h->dy + token * h->dyt * kSize + head * (h->dyh * kSize), c, have, dp);
+                if constexpr (CODED) {
+                    decode8(in[j].x, in[j].byte, v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                dx[i] = r * (g[i] - x[i] * k);
-                if (live) dw[set][i] += d[i] * (x[i] * r);
+                    for (int i = 0; i < 8; ++i)
+                        if (MODE == kAny && i >= have) v[i] = 0.0f;     // a scale that says NaN makes NaNs of the padding
+                } else {
+                    unpack_raw<DT>(in[j].x, v);
+                }
+                double ss[2] = {0.0, 0.0};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    d[i] = __builtin_fmaf(dp[i], sn[i], d[i] * cs[i]);
+                    g[i] = d[i] * (keys ? wk[i] : wq[i]);
+                    const double xd = (double)v[i];
+                    ss[0] = __builtin_fma(xd, xd, ss[0]);
+                    ss[1] = __builtin_fma((double)g[i], xd, ss[1]);
+                }
+                float r = root_of(lanes_sum<L>(ss[0]), t);
+                if (lost) r = bitsf(0x7FC00000u);
+                const float m = (float)((double)r * (double)r * (lanes_sum<L>(ss[1]) * t.inv_dim));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[i] *= r;
+                    o[i] = __builtin_fmaf(-v[i], m, r * g[i]);
+                }
+                store8<DT, MODE != kAny, true>((char *)h->dx + token * h->dxt * kSize + head * (h->dxh * kSize), c, have, o);
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (keys) dw[1][i] = __builtin_fmaf(d[i], v[i], dw[1][i]);
+                        else dw[0][i] = __builtin_fmaf(d[i], v[i], dw[0][i]);
+                    }
+                }
             }
-            store8<DT, MODE == kHalves>(s.dx, token * s.dxt + head * s.dxh + c, n, dx);
         }
     }
-    if (!a.part) return;
-    // the workgroup's sums: the heads of a wave by shuffles, then its waves through LDS, in a fixed order
+    if (!k->part) return;
+    // the workgroup's sums: the heads of a wave by shuffles, then its waves through LDS in binary64, in a fixed order
+    const int wave = wave_id();
 #pragma unroll
     for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
 #pragma unroll
             for (int off = L; off < 64; off <<= 1) dw[q][i] += __shfl_xor(dw[q][i], off, 64);
-            if ((threadIdx.x & 63) < L) comb[threadIdx.x / 64][q][c + i] = dw[q][i];
+            if ((threadIdx.x & 63) < L) comb[wave][q][c + i] = dw[q][i];
         }
     __syncthreads();
-    for (int e = threadIdx.x; e < 2 * t.dim; e += kHeadThreads) {
+    for (int e = threadIdx.x; e < 2 * t.dim; e += kHeadGradThreads) {
         const int q = e >= t.dim, j = e - q * t.dim;
-        float v = comb[0][q][j];
-        for (int w = 1; w < 4; ++w) v += comb[w][q][j];
-        gst<float>(a.part + ((int64_t)blockIdx.x * 2 + q) * t.dim + j, v);
+        double v = (double)comb[0][q][j];
+        for (int w = 1; w < kWaves; ++w) v += (double)comb[w][q][j];
+        gst<float>(k->part + ((int64_t)blockIdx.x * 2 + q) * t.dim + j, (float)v);
     }
 }
 
@@ -279,30 +455,38 @@ __global__ __launch_bounds__(1024) void head_dw_kernel(const float *part, int64_
 
 static int head_lanes(int dim) { return dim <= 64 ? 8 : dim <= 128 ? 16 : dim <= 256 ? 32 : 64; }
 
-static int64_t head_units(int64_t heads_q, int64_t heads_k, int dim)
+static int mode_of(const HeadTurn &t)
 {
-    const int64_t per = 64 / head_lanes(dim);
-    return (heads_q + per - 1) / per + (heads_k + per - 1) / per;
+    if (t.dim % 8 != 0) return kAny;
+    if (t.rot > 0 && t.neighbours) return kNear;
+    return t.rot % 16 != 0 ? kAny : t.dim == 8 * head_lanes(t.dim) ? kWhole : kHalves;
 }
-
-static bool by_halves(const HeadTurn &t) { return t.dim % 8 == 0 && (t.rot == 0 || (!t.neighbours && t.rot % 16 == 0)); }
 
 int64_t head_grad_groups(int64_t tokens, int64_t heads_q, int64_t heads_k, int dim)
 {
-    const int64_t n = (tokens + kHeadThreads / 64 - 1) / (kHeadThreads / 64);
-    return n < 512 ? n : 512;
+    constexpr int kWaves = kHeadGradThreads / 64;
+    const int64_t n = (tokens + kWaves - 1) / kWaves;
+    return n < kHeadGradGroups ? n : kHeadGradGroups;
 }
 
 template <int DT, int L>
 static hipError_t launch_head_t(const HeadArgs &a, hipStream_t st)
 {
-    const int64_t units = head_units(a.s[0].heads, a.s[1].heads, a.t.dim);
-    int64_t per = a.t.tokens * units / 8192;       // 8192 waves fill the chip
-    per = per < 1 ? 1 : per > units ? units : per;
+    constexpr int64_t kUnit = 64 / L, kMost = head_most<DT>();
+    const int64_t units = (a.s[0].heads + kUnit - 1) / kUnit + (a.s[1].heads + kUnit - 1) / kUnit;
+    int64_t per = (units + (units + kMost - 1) / kMost - 1) / ((units + kMost - 1) / kMost);     // as few parts as can be, alike
+    if (per > a.t.tokens * units / 8192) per = a.t.tokens * units / 8192;                          // but waves that fill the chip
+    per = per < 1 ? 1 : per;
     const int64_t waves = a.t.tokens * ((units + per - 1) / per), want = (waves + kHeadThreads / 64 - 1) / (kHeadThreads / 64);
     const unsigned grid = (unsigned)(want < (1 << 20) ? want : 1 << 20);
-    if (by_halves(a.t)) hipLaunchKernelGGL((head_norm_kernel<DT, L, kHalves>), dim3(grid), dim3(kHeadThreads), 0, st, a, (int)per);
-    else hipLaunchKernelGGL((head_norm_kernel<DT, L, kAny>), dim3(grid), dim3(kHeadThreads), 0, st, a, (int)per);
+    const bool codes = a.s[0].q.codes || a.s[1].q.codes;
+#define X(M) \
+    case M: \
+        if (codes) hipLaunchKernelGGL((head_norm_kernel<DT, L, M, true>), dim3(grid), dim3(kHeadThreads), 0, st, a, (int)per); \
+        else hipLaunchKernelGGL((head_norm_kernel<DT, L, M, false>), dim3(grid), dim3(kHeadThreads), 0, st, a, (int)per); \
+        break;
+    switch (mode_of(a.t)) { X(kWhole) X(kHalves) X(kNear) X(kAny) }
+#undef X
     return hipGetLastError();
 }
 
@@ -310,8 +494,12 @@ template <int DT, int L, bool CODED>
 static hipError_t launch_head_grad_t(const HeadGradArgs &a, hipStream_t st)
 {
     const unsigned grid = (unsigned)head_grad_groups(a.t.tokens, a.s[0].heads, a.s[1].heads, a.t.dim);
-    if (by_halves(a.t)) hipLaunchKernelGGL((head_norm_grad_kernel<DT, L, kHalves, CODED>), dim3(grid), dim3(kHeadThreads), 0, st, a);
-    else hipLaunchKernelGGL((head_norm_grad_kernel<DT, L, kAny, CODED>), dim3(grid), dim3(kHeadThreads), 0, st, a);
+    switch (mode_of(a.t)) {
+    case kWhole: hipLaunchKernelGGL((head_norm_grad_kernel<DT, L, kWhole, CODED>), dim3(grid), dim3(kHeadGradThreads), 0, st, a); break;
+    case kHalves: hipLaunchKernelGGL((head_norm_grad_kernel<DT, L, kHalves, CODED>), dim3(grid), dim3(kHeadGradThreads), 0, st, a); break;
+    case kNear: hipLaunchKernelGGL((head_norm_grad_kernel<DT, L, kNear, CODED>), dim3(grid), dim3(kHeadGradThreads), 0, st, a); break;
+    default: hipLaunchKernelGGL((head_norm_grad_kernel<DT, L, kAny, CODED>), dim3(grid), dim3(kHeadGradThreads), 0, st, a);
+    }
     return hipGetLastError();
 }
 

@@ -470,4 +470,30 @@ __device__ __forceinline__ uint32_t top8(const float v[8])
     return fbits(m);
 }
 
+// A kernel's argument record where the launch left it.  A record of many
+// matrices held in scalar registers spills them; read again where it is used
+// (again() forgets what was read) it costs a scalar load.
+#if defined(__HIP_DEVICE_COMPILE__)
+#define OPT_CONST __attribute__((address_space(4)))
+#else
+#define OPT_CONST
+#endif
+
+template <class A>
+__device__ __forceinline__ const OPT_CONST A *kernargs() { return (const OPT_CONST A *)__builtin_amdgcn_kernarg_segment_ptr(); }
+
+template <class A>
+__device__ __forceinline__ const OPT_CONST A *again(const OPT_CONST A *a)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+s"(a));
+#endif
+    return a;
+}
+
+__device__ __forceinline__ Codes copy(const OPT_CONST Codes &q) { return Codes{q.codes, q.ld, q.scales, q.lds}; }
+
+// The wave's number, in a scalar register.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6); }
+
 }  // namespace optstep
