@@ -108,15 +108,20 @@ __device__ __forceinline__ void weights(const HeadTurn &t, const void *w, int c,
         if (c + i < t.rot) vp[i] = load_any(t.w_dtype, w, pair_of<MODE>(t, c + i).partner);
 }
 
-// The partners of a lane's eight elements of a head whose row begins at p.  Every
-// lane of the wave calls it.
-template <int DT, int L, int MODE>
-__device__ __forceinline__ void partners(const HeadTurn &t, const Raw<DT> &raw, const void *p, int c, int cnt, float v[8])
+// Where element `at` of a wave's 512 lies in the LDS: eight apart in every lane,
+// no two lanes share a bank.
+__device__ __forceinline__ int wave_at(int at) { return at + (at >> 6); }
+constexpr int kWaveFloats = 512 + 8;
+
+// The partners of a lane's eight elements of a head.  Every lane of the wave
+// calls it; `lds` is the wave's own (kAny).
+template <int DT, int MODE>
+__device__ __forceinline__ void partners(const HeadTurn &t, const Raw<DT> &raw, int c, float v[8], float *lds)
 {
+    const int lane = threadIdx.x & 63, h = t.rot / 2;
     if (by_halves(MODE)) {
         // the lane h/8 up or down the head; what it holds, as stored
-        const int lane = threadIdx.x & 63, d = t.rot / 16;
-        const int from = 4 * (c >= t.rot ? lane : c < t.rot / 2 ? lane + d : lane - d);
+        const int from = 4 * (c >= t.rot ? lane : c < h ? lane + h / 8 : lane - h / 8);
         Raw<DT> o;
 #pragma unroll
         for (int j = 0; j < (DT == kP32 ? 2 : 1); ++j)
@@ -135,9 +140,20 @@ __device__ __forceinline__ void partners(const HeadTurn &t, const Raw<DT> &raw, 
         }
         return;
     }
+    // by element through the LDS, whose accesses of one wave keep their order
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < cnt && c + i < t.rot) v[i] = load_any(DT, p, pair_of<MODE>(t, c + i).partner);
+    for (int i = 0; i < 8; ++i) lds[wave_at(8 * lane + i)] = v[i];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int e = c + i, d = e >= t.rot ? 0 : e < h ? h : -h;
+        v[i] = lds[wave_at(8 * lane + i + d)];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 __device__ __forceinline__ HeadTurn turn_of(const OPT_CONST HeadTurn &t)
@@ -195,6 +211,7 @@ template <int DT, int L, int MODE, bool CODES>
 __global__ __launch_bounds__(kHeadThreads) void head_norm_kernel(HeadArgs, int)
 {
     constexpr int S = 64 / L, kSize = sizeof(typename Elem<DT>::T), kMost = head_most<DT>();
+    __shared__ float lds[MODE == kAny ? kHeadThreads / 64 * kWaveFloats : 1];
     const OPT_CONST HeadLaunch *k = kernargs<HeadLaunch>();
     const HeadTurn t = turn_of(k->a.t);
     const int per = k->per, lane = threadIdx.x % L, c = 8 * lane, slot = (threadIdx.x & 63) / L;
@@ -252,7 +269,7 @@ __global__ __launch_bounds__(kHeadThreads) void head_norm_kernel(HeadArgs, int)
             const int have = MODE == kWhole ? 8 : live ? cnt : 0;
             float v[8], vp[8], o[8];
             unpack_raw<DT>(raw[j], v);
-            partners<DT, L, MODE>(t, raw[j], (const char *)h->x + token * h->xt * kSize + head * (h->xh * kSize), c, have, vp);
+            partners<DT, MODE>(t, raw[j], c, vp, lds + wave_id() * kWaveFloats);
             double ss = 0.0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss = __builtin_fma((double)v[i], (double)v[i], ss);
@@ -309,6 +326,7 @@ __global__ __launch_bounds__(kHeadGradThreads) void head_norm_grad_kernel(HeadGr
 {
     constexpr int kWaves = kHeadGradThreads / 64, S = 64 / L, kSize = sizeof(typename Elem<DT>::T), kMost = head_grad_most<DT, CODED>();
     __shared__ float comb[kWaves][2][L * 8];
+    __shared__ float lds[MODE == kAny ? kWaves * kWaveFloats : 1];
     const OPT_CONST HeadGradArgs *k = kernargs<HeadGradArgs>();
     const HeadTurn t = turn_of(k->t);
     const int lane = threadIdx.x % L, c = 8 * lane, slot = (threadIdx.x & 63) / L;
@@ -370,7 +388,7 @@ __global__ __launch_bounds__(kHeadGradThreads) void head_norm_grad_kernel(HeadGr
                 const int have = MODE == kWhole ? 8 : live ? cnt : 0;
                 float v[8], d[8], dp[8], g[8], o[8];
                 unpack_raw<DT>(in[j].dy, d);
-                partners<DT, L, MODE>(t, in[j].dy, (const char *)h->dy + token * h->dyt * kSize + head * (h->dyh * kSize), c, have, dp);
+                partners<DT, MODE>(t, in[j].dy, c, dp, lds + wave_id() * kWaveFloats);
                 if constexpr (CODED) {
                     decode8(in[j].x, in[j].byte, v);
 #pragma unroll
