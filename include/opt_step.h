@@ -313,7 +313,9 @@ int opt_round_cast(const float *x, void *out, int64_t n, int32_t out_dtype, int3
 /* ---- the training pass beside the step --------------------------------
  * Operators that produce the gradients the step consumes: dropout from the
  * rounding cast's generator, the root-mean-square norm with the residual's
- * addition, the cast to block-coded matrices, and their product.  They hold no
+ * addition, the cast to block-coded matrices, their product, the gated
+ * activation, the heads' norm with rotation, and what a coded matrix holds (8-bit
+ * checkpoints and their use in the backward passes).  They hold no
  * workspace and take no lock: calls may overlap on any streams, threads and
  * devices (each call runs on the current device, on a stream of that device)
  * and be captured into graphs.
@@ -557,7 +559,9 @@ int opt_block_restore(const opt_restore *a, void *stream);
  *   n = (x * r) * weight;
  *   the first rot elements of n turn in pairs (a, b), elements i and i + rot/2
  *   (interleaved: 2 i and 2 i + 1), to (a c_i - b s_i, b c_i + a s_i), i < rot/2,
- * in binary32, rounded once on store.  c_i and s_i stand in row p of the
+ * in binary32 (x * r, then once each of the pair times weight * c_i and weight
+ * * s_i, and their sum), rounded once on store; r as in opt_rms_norm where
+ * mean(x^2) + eps is tiny.  c_i and s_i stand in row p of the
  * table, p the token's position: c_0 .. c_(rot/2 - 1), then s_0 ... .  A
  * token whose position the table does not hold gets NaNs.  rot = 0: the norm
  * alone (the table is not read).

@@ -447,6 +447,54 @@ def test_head_broadcast_gradient():
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
 
 
+def test_keys_alone():
+    """A set of no heads beside one of some: what the other set gives alone."""
+    import torch
+    import optimizer_step_amd as osa
+    x, dy = (laid(head_data(s, 9, 3, 64, "bf16"), "bf16", "packed") for s in (7, 8))
+    w = dev(1 + 0.1 * data(9, 1, 64, "f32")[0], "f32")
+    none = torch.empty(9, 0, 64, dtype=torch.bfloat16, device="cuda")
+    table = osa.rotation_table(9, 64)
+    outs = []
+    for alone in (True, False):
+        y, dx, dw, q = torch.empty_like(x), torch.empty_like(x), torch.empty(64, device="cuda"), osa.block_buffers(27, 64)
+        other = torch.full((64,), 5.0, device="cuda")
+        if alone:
+            osa.opt_head_norm(x, None, w, table=table, q_out=y, q_codes=q)
+            osa.opt_head_norm_backward(dy, None, x, None, w, table=table, dq=dx, dweight_q=dw)
+        else:
+            osa.opt_head_norm(none, x, None, w, table=table, q_out=none, k_out=y, k_codes=q)
+            osa.opt_head_norm_backward(dy[:, :0], dy, none, x, None, w, table=table, dq=none, dk=dx, dweight_q=other, dweight_k=dw)
+            assert not other.any()
+        outs.append((y, dx, dw, *q))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+def test_readme_block_runs():
+    """The block example of README.md runs as written; its results in 8 bits
+    against the same block in binary32 from the tensors it holds."""
+    import os
+    import re
+    import torch
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    code = re.findall(r"```python\n(.*?)```", text, re.S)[2]
+    torch.manual_seed(0)
+    env = {}
+    exec(compile("import torch, optimizer_step_amd as osa\n" + code, "README.md", "exec"), env)
+    torch.cuda.synchronize()
+    b, inner = env["b"].float(), env["inner"]
+    gate, up = b[:, :inner].cpu().numpy(), b[:, inner:].cpu().numpy()
+    want, bound = G.gate(gate, up, "silu", "bf16")
+    G.check_codes(env["aq"], want, bound, *want.shape)
+    held = [P.decode(q[0].cpu().numpy(), q[1].cpu().numpy()[:, :want.shape[0]], inner) for q in (env["gq"], env["uq"])]
+    (dg, bg), _, _ = G.gate_gradients(env["da"].float().cpu().numpy(), held[0], held[1], "silu", "bf16")
+    G.check_codes((env["bq"][0][:, :inner], env["bq"][1][:inner // 128]), dg, bg, *dg.shape)
+    tokens, heads, dim = env["tokens"], env["heads"], env["dim"]
+    x = env["z"].float().cpu().numpy()[:, :heads * dim].reshape(tokens, heads, dim)
+    want, bound = G.heads(x, np.ones(dim), env["table"].cpu().numpy(), np.arange(tokens), 1e-6, dim, False)
+    G.check_values(host(env["q"]), want, G.stored(want, bound, "bf16"))
+
+
 def test_head_backward_empty():
     import torch
     import optimizer_step_amd as osa
