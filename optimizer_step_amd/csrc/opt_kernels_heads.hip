@@ -73,13 +73,14 @@ __device__ __forceinline__ void angles(const HeadTurn &t, const float *row, int 
         for (int i = 0; i < 8; ++i) sn[i] = p.first != BACK ? -sn[i] : sn[i];
         return;
     }
+    // all loads at once: elements that do not turn read the row's first
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if (c + i >= t.rot) break;
-        const Pair p = pair_of<MODE>(t, c + i);
-        cs[i] = gld<float>(row + p.index);
-        sn[i] = gld<float>(row + t.rot / 2 + p.index);
-        sn[i] = p.first != BACK ? -sn[i] : sn[i];
+        const bool turns = c + i < t.rot;
+        const Pair p = pair_of<MODE>(t, turns ? c + i : 0);
+        const float x = gld<float>(row + p.index), y = gld<float>(row + t.rot / 2 + p.index);
+        cs[i] = turns ? x : 1.0f;
+        sn[i] = turns ? (p.first != BACK ? -y : y) : 0.0f;
     }
 }
 
@@ -104,8 +105,10 @@ __device__ __forceinline__ void weights(const HeadTurn &t, const void *w, int c,
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (c + i < t.rot) vp[i] = load_any(t.w_dtype, w, pair_of<MODE>(t, c + i).partner);
+    for (int i = 0; i < 8; ++i) {
+        if (MODE == kNear) vp[i] = v[i ^ 1];
+        else vp[i] = load_any(t.w_dtype, w, c + i < t.rot ? pair_of<MODE>(t, c + i).partner : 0);
+    }
 }
 
 // Where element `at` of a wave's 512 lies in the LDS: eight apart in every lane,
