@@ -11,6 +11,7 @@ Tensors are passed as a list of dicts with torch CUDA tensors under the keys
 """
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libopt_step.so")
@@ -189,7 +190,7 @@ def lib():
             "opt_gated_act": ([ctypes.POINTER(OptGate), vp], i32),
             "opt_gated_act_backward": ([ctypes.POINTER(OptGateGrad), vp], i32),
             "opt_block_restore": ([ctypes.POINTER(OptRestore), vp], i32),
-            "opt_head_norm": ([ctypes.POINTER(OptHeads), vp], i32),
+            "opt_head_norm": ([vp, vp], i32),
             "opt_head_norm_workspace": ([i64, i64, i64, i32], i64),
             "opt_head_norm_backward": ([ctypes.POINTER(OptHeadsGrad), vp], i32),
             "opt_debug_mini_host": ([i32, ctypes.c_float, vp, vp, vp, vp, i64], i32),
@@ -835,6 +836,13 @@ def rotation_table(positions, rot, base=10000.0, device="cuda"):
     return torch.cat([a.cos(), a.sin()], 1).float()
 
 
+# opt_heads as one record of plain fields: half the time of its ctypes classes,
+# which a call for one token is mostly made of
+_HEADS = struct.Struct("<q6id" + "Qqq" + "Q2i" + 2 * "qQqqQQqqQqQq")
+_NO_HEADS = (0,) * 12
+_NO_TABLE = (0, 0, 0, 0, 64, 0)
+
+
 def _head_rows(t, what, like, shape, dev):
     """(pointer, stride of a token, stride of a head) of heads [tokens, heads,
     dim] whose elements are neighbours."""
@@ -853,9 +861,9 @@ def _head_rows(t, what, like, shape, dev):
 
 
 def _head_table(table, positions, tokens, dev):
-    """(the record, rot) of a rotation's table and positions."""
+    """(the fields of its record, rot) of a rotation's table and positions."""
     if table is None:
-        return OptHeadTable(None, 0, 0, None, 64, 0), 0
+        return _NO_TABLE, 0
     import torch
     _on_device(table, "table", dev)
     if table.dtype != torch.float32 or table.dim() != 2 or (table.stride(1) != 1 and table.shape[1] > 1):
@@ -863,23 +871,23 @@ def _head_table(table, positions, tokens, dev):
     rows, rot = table.shape
     ld = table.stride(0) if rows > 1 else rot
     if positions is None:
-        return OptHeadTable(table.data_ptr(), rows, ld, None, 64, 0), rot
+        return (table.data_ptr(), rows, ld, 0, 64, 0), rot
     _on_device(positions, "positions", dev)
     bits = 64 if positions.dtype == torch.int64 else 32
     if (bits == 32 and positions.dtype != torch.int32) or positions.numel() != tokens or not positions.is_contiguous():
         raise ValueError(f"positions must be {tokens} contiguous int64 or int32")
-    return OptHeadTable(table.data_ptr(), rows, ld, positions.data_ptr(), bits, 0), rot
+    return (table.data_ptr(), rows, ld, positions.data_ptr(), bits, 0), rot
 
 
 def _head_weights(weight_q, weight_k, dim, dev):
     """(pointer, pointer, type) of the two sets' weights, either None."""
-    pq = pk = None
+    pq = pk = 0
     dt = OPT_F32
     if weight_q is not None:
         pq, dt = _weight(weight_q, dim, dev)
     if weight_k is not None:
         pk, dk = _weight(weight_k, dim, dev)
-        if pq is not None and dk != dt:
+        if pq and dk != dt:
             raise ValueError("weight_q and weight_k must be of one type")
         dt = dk
     return pq, pk, dt
@@ -905,17 +913,25 @@ def opt_head_norm(q, k, weight_q=None, weight_k=None, table=None, positions=None
     tokens, heads, dim = shape
     tab, rot = _head_table(table, positions, tokens, dev)
     pwq, pwk, wd = _head_weights(weight_q, weight_k, dim, dev)
-    sq = OptHeadSet(heads, *_head_rows(q, "q", dtype, shape, dev), pwq, *_head_rows(q_out, "q_out", dtype, shape, dev),
-                    _coded(q_codes, "q_codes'", tokens * heads, dim, dev))
-    sk = OptHeadSet()
-    if k is not None:
-        if k.dim() != 3 or k.shape[0] != tokens or k.shape[2] != dim:
-            raise ValueError(f"k must be [{tokens}, heads, {dim}], got {list(k.shape)}")
-        shape = k.shape
-        sk = OptHeadSet(shape[1], *_head_rows(k, "k", dtype, shape, dev), pwk, *_head_rows(k_out, "k_out", dtype, shape, dev),
-                        _coded(k_codes, "k_codes'", tokens * shape[1], dim, dev))
-    a = OptHeads(tokens, dim, rot, _type(q), wd, 1 if interleaved else 0, 0, float(eps), tab, sq, sk)
-    return _check((_lib or lib()).opt_head_norm(ctypes.byref(a), _raw_stream(stream, dev)))
+    sets = []
+    for x, out, w, codes, name in ((q, q_out, pwq, q_codes, "q"), (k, k_out, pwk, k_codes, "k")):
+        if x is None:
+            sets += _NO_HEADS
+            continue
+        shape = x.shape
+        if len(shape) != 3 or shape[0] != tokens or shape[2] != dim:
+            raise ValueError(f"{name} must be [{tokens}, heads, {dim}], got {list(shape)}")
+        n = shape[1]
+        px, xt, xh = _head_rows(x, name, dtype, shape, dev)
+        py, yt, yh = _head_rows(out, name + "_out", dtype, shape, dev)
+        sets += (n, px, xt, xh, w, py, yt, yh)
+        if codes is None:
+            sets += (0, 0, 0, 0)
+        else:
+            c = _coded(codes, name + "_codes'", tokens * n, dim, dev)
+            sets += (c.codes or 0, c.ld, c.scales or 0, c.lds)
+    a = _HEADS.pack(tokens, dim, rot, _type(q), wd, 1 if interleaved else 0, 0, float(eps), *tab, *sets)
+    return _check((_lib or lib()).opt_head_norm(a, _raw_stream(stream, dev)))
 
 
 def opt_head_norm_workspace(tokens, heads_q, heads_k, dim):
@@ -973,7 +989,7 @@ def opt_head_norm_backward(dq_out, dk_out, q, k, weight_q=None, weight_k=None, t
             workspace = _scratch(need, stream)
         else:
             _device_buffer(workspace, 1, need, "workspace")
-    a = OptHeadsGrad(tokens, dim, rot, _type(dq_out), wd, 1 if interleaved else 0, 1 if accumulate else 0, float(eps), tab, sq, sk,
+    a = OptHeadsGrad(tokens, dim, rot, _type(dq_out), wd, 1 if interleaved else 0, 1 if accumulate else 0, float(eps), OptHeadTable(*tab), sq, sk,
                      _ptr(workspace) if need else None, need)
     return _check((_lib or lib()).opt_head_norm_backward(ctypes.byref(a), _raw_stream(stream, dev)))
 

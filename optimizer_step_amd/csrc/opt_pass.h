@@ -1,7 +1,8 @@
 // opt_pass.h -- what the training-pass operators beside the step share:
-// dropout, the RMS norm, the cast to block-coded matrices and their product.
-// Kernel argument records, loads and stores of eight elements, and the
-// encoder of one 128-element block.
+// dropout, the RMS norm, the cast to block-coded matrices, their product, the
+// gated activation, the heads' norm and restored codes.  Kernel argument
+// records, loads and stores of eight elements, sums over lanes, and the codecs of
+// one 128-element block.
 #pragma once
 
 #include "opt_device.h"

@@ -336,3 +336,16 @@ def test_code_check_catches_mistakes():
         p[1][1, 3] += d
         with pytest.raises(AssertionError):
             G.check_codes(p, x, np.zeros_like(x), 5, 200)
+
+
+def test_packed_head_record(L):
+    """The binding's packed opt_heads has the fields of its ctypes class, in their places."""
+    values = [7, 1, 2, 3, 4, 5, 6, 0.5, 11, 12, 13, 14, 15, 16, *range(20, 44)]
+    r = L.OptHeads.from_buffer_copy(L._HEADS.pack(*values))
+
+    def flat(s):
+        for name, kind in s._fields_:
+            v = getattr(s, name)
+            yield from flat(v) if isinstance(v, ctypes.Structure) else [v]
+
+    assert list(flat(r)) == values
