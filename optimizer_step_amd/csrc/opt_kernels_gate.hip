@@ -170,11 +170,12 @@ __global__ __launch_bounds__(256) void gated_act_grad_rows_kernel(GateGradArgs a
 // 512 threads: thread t holds the eight columns of group t % 16 in the four
 // rows of group t / 16.  The backward pass forms dgate first, then dup and y
 // together from the inputs again, which stay as they are stored: 128 registers
-// and two workgroups a compute unit.  Measured against 172 us: all three held
-// at once (250 registers, one workgroup) 230, or in 128 registers 642 (spills);
-// s(gate) kept from part to part for two rows 175 (spills); every thread forming
-// its columns' scales, one barrier less a part, 171; a persistent grid 188, with
-// the next tile's loads ahead 215 (spills); tiles down the columns first 200.
+// and two workgroups a compute unit.  Beside 165 to 169 us in the same runs: all
+// three held at once (250 registers, one workgroup) 230, or in 128 registers 642
+// (spills); s(gate) kept from part to part for two rows 175 (spills); every thread
+// forming its columns' scales, one barrier less a part, 171; a persistent grid
+// 181, with the next tile's loads ahead 215 (spills); tiles down the columns
+// first 200.
 
 constexpr int kTileThreads = 512;
 
