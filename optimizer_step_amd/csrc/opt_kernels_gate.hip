@@ -313,6 +313,7 @@ __device__ __forceinline__ CodedRows load_coded(const Codes &q, int64_t r0, int6
         if (i < live) x.code[i] = gld<u2>(at.row(i));
     }
     if (live > 0) x.bytes = gld<uint32_t>(q.scales + (c0 / kCodeBlock) * q.lds + r0 + 4 * (threadIdx.x >> 4));
+    if (live < 4) x.bytes &= (1u << (8 * live)) - 1u;      // what stands past the last row is nobody's
     return x;
 }
 

@@ -211,6 +211,30 @@ def test_gated_act_backward_lost_block():
         assert not q[np.repeat(bad.T, 128, 1)[:, :q.shape[1]]].any()
 
 
+@pytest.mark.parametrize("rows,cols", [(1, 8), (5, 128), (129, 256), (130, 300), (131, 1000)])
+def test_nobodys_scales(rows, cols):
+    """Scale bytes past the last row, up to the multiple of four, may hold anything (NaN's here)."""
+    import torch
+    import optimizer_step_amd as osa
+    x, u, dy = gate_inputs(rows, cols, "bf16")
+    (gx, _), (gu, _) = coded(x), coded(u)
+    dyd, outs = dev(dy, "bf16"), []
+    for fill in (0, 255):
+        for pair in (gx, gu):
+            pair[1][:, rows:] = fill
+        keys = ("dgate_codes", "dup_codes", "dgate_codes_t", "dup_codes_t", "y_codes_t")
+        pairs = {k: osa.block_buffers(*((cols, rows) if k.endswith("_t") else (rows, cols))) for k in keys}
+        dg, qt, back = empty(rows, cols, "bf16"), osa.block_buffers(cols, rows), empty(rows, cols, "bf16")
+        osa.opt_gated_act_backward(dyd, gx, gu, dgate=dg, **pairs)
+        osa.opt_block_restore(gx, out=back, codes_t=qt)
+        heads, hq = dev(dy, "bf16").view(rows, 1, cols), gx
+        dx, dw = torch.zeros_like(heads), torch.zeros(cols, device="cuda")
+        if cols <= 512:
+            osa.opt_head_norm_backward(heads, None, hq, None, dq=dx, dweight_q=dw)
+        outs.append([dg, back, dx, dw, *qt, *(t for v in pairs.values() for t in v)])
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
 # ---- restored codes ---------------------------------------------------------
 
 
