@@ -564,7 +564,8 @@ int opt_block_restore(const opt_restore *a, void *stream);
  * mean(x^2) + eps is tiny.  c_i and s_i stand in row p of the
  * table, p the token's position: c_0 .. c_(rot/2 - 1), then s_0 ... .  A
  * token whose position the table does not hold gets NaNs.  rot = 0: the norm
- * alone (the table is not read).
+ * alone (the table is not read).  An element past rot is its n, whatever the
+ * elements beside it hold.
  * Strides count elements: element j of head h of token t is x[t*x_token +
  * h*x_head + j].  Any non-negative input strides; outputs keep their heads
  * apart, either all heads of a token before the next token's or the other way

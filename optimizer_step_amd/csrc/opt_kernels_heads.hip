@@ -54,6 +54,10 @@ __device__ __forceinline__ Pair pair_of(const HeadTurn &t, int e)
     return Pair{e < h ? e + h : e - h, e < h ? e : e - h, e < h};
 }
 
+// Whether element c + i turns (rot and c are even: the two of a pair of
+// neighbours alike, so that half as many masks are kept).
+__device__ __forceinline__ bool turns(const HeadTurn &t, int c, int i) { return c + (i & ~1) < t.rot; }
+
 // cos and sin of the eight elements from c on, the sine with the sign of what
 // the partner adds (BACK: turned the other way); 1 and 0 where nothing turns.
 template <int MODE, bool BACK>
@@ -76,11 +80,11 @@ __device__ __forceinline__ void angles(const HeadTurn &t, const float *row, int 
     // all loads at once: elements that do not turn read the row's first
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const bool turns = c + i < t.rot;
-        const Pair p = pair_of<MODE>(t, turns ? c + i : 0);
+        const bool on = turns(t, c, i);
+        const Pair p = pair_of<MODE>(t, on ? c + i : 0);
         const float x = gld<float>(row + p.index), y = gld<float>(row + t.rot / 2 + p.index);
-        cs[i] = turns ? x : 1.0f;
-        sn[i] = turns ? (p.first != BACK ? -y : y) : 0.0f;
+        cs[i] = on ? x : 1.0f;
+        sn[i] = on ? (p.first != BACK ? -y : y) : 0.0f;
     }
 }
 
@@ -91,7 +95,8 @@ __device__ __forceinline__ float load_any(int dt, const void *p, int64_t j)
     return dt == kPBF16 ? bf16_lo(b) : f16_lo(b);
 }
 
-// The weights of the eight elements from c on, and (PARTNERS) of their partners.
+// The weights of the eight elements from c on, and (PARTNERS) of their partners
+// (1 where nothing turns: an infinite weight keeps to its own element).
 template <int MODE, bool PARTNERS>
 __device__ __forceinline__ void weights(const HeadTurn &t, const void *w, int c, int cnt, float v[8], float vp[8])
 {
@@ -106,8 +111,9 @@ __device__ __forceinline__ void weights(const HeadTurn &t, const void *w, int c,
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if (MODE == kNear) vp[i] = v[i ^ 1];
-        else vp[i] = load_any(t.w_dtype, w, c + i < t.rot ? pair_of<MODE>(t, c + i).partner : 0);
+        const bool on = turns(t, c, i);
+        const float x = MODE == kNear ? v[i ^ 1] : load_any(t.w_dtype, w, on ? pair_of<MODE>(t, c + i).partner : 0);
+        vp[i] = on ? x : 1.0f;
     }
 }
 
@@ -116,8 +122,10 @@ __device__ __forceinline__ void weights(const HeadTurn &t, const void *w, int c,
 __device__ __forceinline__ int wave_at(int at) { return at + (at >> 6); }
 constexpr int kWaveFloats = 512 + 8;
 
-// The partners of a lane's eight elements of a head.  Every lane of the wave
-// calls it; `lds` is the wave's own (kAny).
+// The partners of a lane's eight elements of a head; zeros where nothing turns,
+// so that an infinity or a NaN there keeps to its own element (its partner's
+// angle is 0, but infinity times 0 is NaN).  Every lane of the wave calls it;
+// `lds` is the wave's own (kAny).
 template <int DT, int MODE>
 __device__ __forceinline__ void partners(const HeadTurn &t, const Raw<DT> &raw, int c, float v[8], float *lds)
 {
@@ -130,6 +138,10 @@ __device__ __forceinline__ void partners(const HeadTurn &t, const Raw<DT> &raw, 
         for (int j = 0; j < (DT == kP32 ? 2 : 1); ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o.v[j][i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)raw.v[j][i]);
+        if (t.rot < t.dim && c >= t.rot) {         // (whole rotations skip it)
+#pragma unroll
+            for (int j = 0; j < (DT == kP32 ? 2 : 1); ++j) o.v[j] = (u4){0u, 0u, 0u, 0u};
+        }
         unpack_raw<DT>(o, v);
         return;
     }
@@ -138,8 +150,8 @@ __device__ __forceinline__ void partners(const HeadTurn &t, const Raw<DT> &raw, 
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
             const float x = v[i];
-            v[i] = v[i + 1];
-            v[i + 1] = x;
+            v[i] = turns(t, c, i) ? v[i + 1] : 0.0f;
+            v[i + 1] = turns(t, c, i) ? x : 0.0f;
         }
         return;
     }
@@ -152,7 +164,8 @@ __device__ __forceinline__ void partners(const HeadTurn &t, const Raw<DT> &raw, 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int e = c + i, d = e >= t.rot ? 0 : e < h ? h : -h;
-        v[i] = lds[wave_at(8 * lane + i + d)];
+        const float x = lds[wave_at(8 * lane + i + d)];
+        v[i] = turns(t, c, i) ? x : 0.0f;
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -279,7 +292,11 @@ __global__ __launch_bounds__(kHeadThreads) void head_norm_kernel(HeadArgs, int)
             float r = root_of(lanes_sum<L>(ss), t);
             if (lost) r = bitsf(0x7FC00000u);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = __builtin_fmaf(vp[i] * r, B[0][i], (v[i] * r) * A[0][i]);
+            for (int i = 0; i < 8; ++i) {
+                // an infinite r (a head of tiny elements) times the zero of an element that does not turn: NaN
+                const float rp = turns(t, c, by_halves(MODE) ? 0 : i) ? r : 0.0f;
+                o[i] = __builtin_fmaf(vp[i] * rp, B[0][i], (v[i] * r) * A[0][i]);
+            }
             store8<DT, MODE != kAny, true>((char *)h->y + token * h->yt * kSize + head * (h->yh * kSize), c, have, o);
             if (CODES && h->q.codes) {
                 const Codes q = copy(h->q);

@@ -1,0 +1,83 @@
+"""GPU tests of the operators between a layer's products at the ends of their
+ranges: values that are not finite, and what they may reach."""
+import numpy as np
+import pytest
+
+from tests import layer_plain as G
+from tests import pass_plain as P
+from tests.test_gpu_layer import coded, gpu, head_data, head_out, laid  # noqa: F401 (gpu: a fixture)
+from tests.test_gpu_pass import dev, host
+
+pytestmark = pytest.mark.gpu
+
+# dim, rot, neighbouring pairs: part of a head turned, for each way a pair is found (whole and unfilled lanes, by lanes, within a
+# lane, element by element, an end inside a lane's eight), and nothing turned
+PARTS = [(128, 64, False), (96, 64, False), (64, 32, True), (64, 12, True), (80, 6, True), (128, 20, False), (100, 20, False), (7, 4, False),
+         (7, 4, True), (128, 0, False), (100, 0, False)]
+
+
+@pytest.mark.parametrize("dim,rot,near", PARTS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_infinity_beyond_the_rotation(dim, rot, near, dtype):
+    """An infinite element or weight that does not turn reaches no other element."""
+    import torch
+    import optimizer_step_amd as osa
+    x = head_data(dim, 4, 5, dim, dtype)
+    x[0, 0, rot + 1] = np.inf                       # its neighbour does not turn either
+    x[1, 4, dim - 1] = -np.inf
+    w = P.rounded(0.5 + np.random.RandomState(dim).rand(dim), dtype)
+    tab, pos = G.table(50, max(rot, 2)), np.array([3, 9, 20, 49])
+    kw = dict(table=torch.from_numpy(tab).cuda() if rot else None, positions=torch.from_numpy(pos).cuda(), interleaved=near)
+    for at in (None, rot + 1, dim - 1, 0):          # an infinite weight too
+        v = w.copy()
+        if at is not None:
+            v[at] = np.inf
+        y = head_out(4, 5, dim, dtype, "packed")
+        osa.opt_head_norm(laid(x, dtype, "packed"), None, dev(v, dtype), q_out=y, **kw)
+        with np.errstate(invalid="ignore"):
+            want, bound = G.heads(x, v, tab, pos, 1e-6, rot, near)
+        G.check_values(host(y), want, np.where(np.isfinite(want), G.stored(want, bound, dtype), 0))
+
+
+@pytest.mark.parametrize("dim,rot,near", PARTS)
+def test_tiny_heads_beyond_the_rotation(dim, rot, near):
+    """Where r is infinite an element that does not turn is infinite, or NaN if it is zero."""
+    import torch
+    import optimizer_step_amd as osa
+    x = np.where(np.arange(2 * 3 * dim).reshape(2, 3, dim) % 3 == 0, -1e-40, 1e-40).astype(np.float32)
+    x[0, 1, dim - 1] = 0
+    y = head_out(2, 3, dim, "f32", "packed")
+    tab = torch.from_numpy(G.table(9, max(rot, 2))).cuda() if rot else None
+    osa.opt_head_norm(laid(x, "f32", "packed"), None, table=tab, eps=0.0, interleaved=near, q_out=y)
+    want = np.where(x == 0, np.nan, np.copysign(np.inf, x))[..., rot:]
+    assert np.array_equal(host(y)[..., rot:], want, equal_nan=True)
+
+
+@pytest.mark.parametrize("dim,rot,near", PARTS)
+@pytest.mark.parametrize("dtype,from_codes", [("f32", False), ("bf16", True), ("f16", False)])
+def test_infinite_gradient_beyond_the_rotation(dim, rot, near, dtype, from_codes):
+    """A gradient that is not finite, of an element that does not turn, reaches its own head's dx and its own dweight alone."""
+    import torch
+    import optimizer_step_amd as osa
+    x, dy = head_data(dim, 6, 3, dim, dtype), head_data(dim + 1, 6, 3, dim, dtype, 0.1)
+    dy[0, 0, rot + 1] = np.inf
+    dy[1, 2, dim - 1] = np.nan
+    dy[2, 1, rot + 1] = np.inf
+    x[0, 0, rot + 1] = x[2, 1, rot + 1] = 0.75      # the two infinities have one sign in dweight
+    w = P.rounded(0.5 + np.random.RandomState(dim).rand(dim), "f32")
+    tab, pos = G.table(50, max(rot, 2)), np.array([3, 9, 20, 49, 1, 7])
+    if from_codes:
+        xin, held = coded(x.reshape(-1, dim))
+        x = held.reshape(x.shape)
+    else:
+        xin = laid(x, dtype, "packed")
+    dx, dw = head_out(6, 3, dim, dtype, "packed"), torch.zeros(dim, device="cuda")
+    osa.opt_head_norm_backward(laid(dy, dtype, "packed"), None, xin, None, dev(w, "f32"), interleaved=near, dq=dx, dweight_q=dw,
+                               table=torch.from_numpy(tab).cuda() if rot else None, positions=torch.from_numpy(pos).cuda())
+    with np.errstate(invalid="ignore"):
+        (want, bound), (want_w, terms) = G.head_gradients(dy, x, w, tab, pos, 1e-6, rot, near)
+    bad = np.arange(dim) == dim - 1
+    assert np.isnan(want_w[bad]).all() and np.isfinite(want_w[~bad]).sum() == dim - 2 and np.isinf(want_w[rot + 1])
+    G.check_values(host(dx), want, np.where(np.isfinite(want), G.stored(want, bound, dtype), 0))
+    # dn and x r to 4 units, r to 1; 18 heads' terms added
+    G.check_values(host(dw), want_w, np.where(np.isfinite(want_w), (5 + 18) * P.U32 * terms * 1.05, 0))
