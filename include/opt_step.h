@@ -610,11 +610,11 @@ int opt_head_norm(const opt_heads *a, void *stream);
  *   c = mean(g * x)  (both sums of a head in binary64),
  *   dx = r * (g - x * (r^2 c)),
  *   dweight = sum over tokens and heads of dn * (x * r).
- * The sums over tokens run in a fixed order (no atomics): binary32 within a
- * workgroup's heads, binary64 across workgroups.  dx may be dy with the same
- * strides.  A token whose position the table does not hold gets NaNs, and they
- * reach dweight.  With no heads or tokens a dweight becomes 0 (or stays, with
- * accumulate). */
+ * The sums over tokens run in a fixed order (no atomics): binary32 over at most
+ * 32 heads in turn, binary64 from there on, rounded once to dweight.  dx may be
+ * dy with the same strides.  A token whose position the table does not hold gets
+ * NaNs, and they reach dweight.  With no heads or tokens a dweight becomes 0 (or
+ * stays, with accumulate). */
 typedef struct {
     int64_t heads;             /* 0 for none                                           */
     const void *dy;

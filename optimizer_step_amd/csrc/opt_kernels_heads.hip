@@ -311,7 +311,9 @@ __global__ __launch_bounds__(kHeadThreads) void head_norm_kernel(HeadArgs, int)
 }
 
 // The backward pass: a wave takes tokens in turn and keeps its sums of both
-// weights' gradients in registers.
+// weights' gradients in registers, in binary32 over 32 units at most, then joins
+// them to its sums in the LDS, in binary64 from there on (all of a wave's sums in
+// binary64 registers would cost a wave a SIMD).
 constexpr int kHeadGradThreads = 256;
 constexpr int64_t kHeadGradGroups = 1024;    // four waves a SIMD; 512 measured 72 us against 55 at the sizes above
 
@@ -339,19 +341,39 @@ __device__ __forceinline__ void arrived(HeadIn<DT, true> (&x)[N])
     }
 }
 
+constexpr int kHeadFold = 32;
+
 template <int DT, bool CODED> constexpr int head_grad_most() { return DT == kP32 ? 2 : 4; }
 
 template <int DT, int L, int MODE, bool CODED>
 __global__ __launch_bounds__(kHeadGradThreads) void head_norm_grad_kernel(HeadGradArgs)
 {
     constexpr int kWaves = kHeadGradThreads / 64, S = 64 / L, kSize = sizeof(typename Elem<DT>::T), kMost = head_grad_most<DT, CODED>();
-    __shared__ float comb[kWaves][2][L * 8];
+    __shared__ double comb[kWaves][2][L * 8];
     __shared__ float lds[MODE == kAny ? kWaves * kWaveFloats : 1];
     const OPT_CONST HeadGradArgs *k = kernargs<HeadGradArgs>();
     const HeadTurn t = turn_of(k->t);
     const int lane = threadIdx.x % L, c = 8 * lane, slot = (threadIdx.x & 63) / L;
     const int cnt = left8(c, t.dim);
+    const int wave = wave_id();
     float dw[2][8] = {};
+    int summed = 0;        // units since the sums last joined the LDS's, where lane l < L owns columns 8 l on of its wave's
+    if (slot == 0)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) comb[wave][0][c + i] = comb[wave][1][c + i] = 0.0;
+    auto join = [&] {
+        int at = c;
+        asm volatile("" : "+v"(at));               // no address is kept for this in the loop
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const double v = groups_sum<L>((double)dw[q][i]);
+                if (slot == 0) comb[wave][q][at + i] += v;
+                dw[q][i] = 0.0f;
+            }
+        summed = 0;
+    };
     const int64_t step = (int64_t)gridDim.x * kWaves;
     const int headsq = (int)k->s[0].heads, headsk = (int)k->s[1].heads;
     const int unitsq = (headsq + S - 1) / S, units = unitsq + (headsk + S - 1) / S;
@@ -443,39 +465,34 @@ __global__ __launch_bounds__(kHeadGradThreads) void head_norm_grad_kernel(HeadGr
                     }
                 }
             }
+            summed += n;
+            if (summed > kHeadFold - kMost && k->part) join();
         }
     }
     if (!k->part) return;
-    // the workgroup's sums: the heads of a wave by shuffles, then its waves through LDS in binary64, in a fixed order
-    const int wave = wave_id();
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-#pragma unroll
-            for (int off = L; off < 64; off <<= 1) dw[q][i] += __shfl_xor(dw[q][i], off, 64);
-            if ((threadIdx.x & 63) < L) comb[wave][q][c + i] = dw[q][i];
-        }
+    // the workgroup's sums: its waves' in a fixed order
+    join();
     __syncthreads();
     for (int e = threadIdx.x; e < 2 * t.dim; e += kHeadGradThreads) {
         const int q = e >= t.dim, j = e - q * t.dim;
-        double v = (double)comb[0][q][j];
-        for (int w = 1; w < kWaves; ++w) v += (double)comb[w][q][j];
-        gst<float>(k->part + ((int64_t)blockIdx.x * 2 + q) * t.dim + j, (float)v);
+        double v = comb[0][q][j];
+        for (int w = 1; w < kWaves; ++w) v += comb[w][q][j];
+        gst<double>(k->part + ((int64_t)blockIdx.x * 2 + q) * t.dim + j, v);
     }
 }
 
-// dw[c] (+)= sum over the groups' partials, in binary64 and a fixed order: 32
-// columns a workgroup, 32 half-waves every 32nd group each.
-__global__ __launch_bounds__(1024) void head_dw_kernel(const float *part, int64_t groups, int dim, float *dwq, float *dwk, int accumulate)
+// dw[c] (+)= sum over the groups' partials, in binary64 and a fixed order: 16
+// columns a workgroup, 64 quarter-waves every 64th group each (2 x 128 columns of
+// 1024 groups: 4.9 us; 32 columns 5.6).
+__global__ __launch_bounds__(1024) void head_dw_kernel(const double *part, int64_t groups, int dim, float *dwq, float *dwk, int accumulate)
 {
-    __shared__ double s[32][32];
-    const int lane = threadIdx.x % 32, rank = threadIdx.x / 32;
-    const int e = (int)blockIdx.x * 32 + lane;
+    __shared__ double s[64][16];
+    const int lane = threadIdx.x % 16, rank = threadIdx.x / 16;
+    const int e = (int)blockIdx.x * 16 + lane;
     double v = 0.0;
     if (e < 2 * dim) {
-#pragma unroll 4
-        for (int64_t g = rank; g < groups; g += 32) v += (double)gld<float>(part + g * 2 * dim + e);
+#pragma unroll 16
+        for (int64_t g = rank; g < groups; g += 64) v += gld<double>(part + g * 2 * dim + e);
     }
     s[rank][lane] = v;
     __syncthreads();
@@ -483,7 +500,7 @@ __global__ __launch_bounds__(1024) void head_dw_kernel(const float *part, int64_
         float *dw = e < dim ? dwq : dwk;
         if (!dw) return;
         const int j = e < dim ? e : e - dim;
-        for (int i = 1; i < 32; ++i) v += s[i][lane];
+        for (int i = 1; i < 64; ++i) v += s[i][lane];
         if (accumulate) v += (double)gld<float>(dw + j);
         gst<float>(dw + j, (float)v);
     }
@@ -581,7 +598,7 @@ hipError_t launch_head_norm_grad(int dt, int coded, const HeadGradArgs &a, float
     }
     if (e != hipSuccess || (!dwq && !dwk)) return e;
     const int64_t groups = any ? head_grad_groups(a.t.tokens, a.s[0].heads, a.s[1].heads, a.t.dim) : 0;
-    hipLaunchKernelGGL(head_dw_kernel, dim3((unsigned)((2 * a.t.dim + 31) / 32)), dim3(1024), 0, st, (const float *)a.part, groups, a.t.dim, dwq, dwk,
+    hipLaunchKernelGGL(head_dw_kernel, dim3((unsigned)((2 * a.t.dim + 15) / 16)), dim3(1024), 0, st, (const double *)a.part, groups, a.t.dim, dwq, dwk,
                        accumulate);
     return hipGetLastError();
 }

@@ -130,7 +130,7 @@ struct HeadArgs {
 struct HeadGradArgs {
     HeadTurn t;
     HeadGradSet s[2];
-    float *part;           // [groups][2][dim] partial sums of the weights' gradients, or null
+    double *part;          // [groups][2][dim] partial sums of the weights' gradients, or null
 };
 
 int64_t head_grad_groups(int64_t tokens, int64_t heads_q, int64_t heads_k, int dim);
@@ -305,6 +305,23 @@ __device__ __forceinline__ double dpp_add(double x)
                          (uint32_t)__builtin_amdgcn_mov_dpp((int)hi, CTRL, 0xF, 0xF, true));
 }
 
+// x of both lanes of a pair 16 lanes apart (within a half of the wave), 32 lanes apart.
+__device__ __forceinline__ double swap16_add(double x)
+{
+    const uint32_t lo = (uint32_t)__double2loint(x), hi = (uint32_t)__double2hiint(x);
+    const auto l = __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+    const auto h = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+    return two_words(l[0], h[0]) + two_words(l[1], h[1]);
+}
+
+__device__ __forceinline__ double swap32_add(double x)
+{
+    const uint32_t lo = (uint32_t)__double2loint(x), hi = (uint32_t)__double2hiint(x);
+    const auto l = __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
+    const auto h = __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+    return two_words(l[0], h[0]) + two_words(l[1], h[1]);
+}
+
 // Sum over 8, 16, 32 or 64 lanes, the same bits in every lane: each step adds
 // two partial sums that both sides hold (lanes 1, 2, 7 - i and 15 - i away by
 // DPP; then the rows and the halves of the wave by gfx950's lane swaps).
@@ -315,18 +332,18 @@ __device__ __forceinline__ double lanes_sum(double x)
     x = dpp_add<0x4E>(x);
     x = dpp_add<0x141>(x);
     if (LANES >= 16) x = dpp_add<0x140>(x);
-    if (LANES >= 32) {
-        const uint32_t lo = (uint32_t)__double2loint(x), hi = (uint32_t)__double2hiint(x);
-        const auto l = __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
-        const auto h = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
-        x = two_words(l[0], h[0]) + two_words(l[1], h[1]);
-    }
-    if (LANES >= 64) {
-        const uint32_t lo = (uint32_t)__double2loint(x), hi = (uint32_t)__double2hiint(x);
-        const auto l = __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
-        const auto h = __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
-        x = two_words(l[0], h[0]) + two_words(l[1], h[1]);
-    }
+    if (LANES >= 32) x = swap16_add(x);
+    if (LANES >= 64) x = swap32_add(x);
+    return x;
+}
+
+// The rest of a wave's sum: over the 64/LANES lanes that are LANES apart.
+template <int LANES>
+__device__ __forceinline__ double groups_sum(double x)
+{
+    if (LANES <= 8) x = dpp_add<0x128>(x);
+    if (LANES <= 16) x = swap16_add(x);
+    if (LANES <= 32) x = swap32_add(x);
     return x;
 }
 

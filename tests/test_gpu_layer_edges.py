@@ -81,3 +81,29 @@ def test_infinite_gradient_beyond_the_rotation(dim, rot, near, dtype, from_codes
     G.check_values(host(dx), want, np.where(np.isfinite(want), G.stored(want, bound, dtype), 0))
     # dn and x r to 4 units, r to 1; 18 heads' terms added
     G.check_values(host(dw), want_w, np.where(np.isfinite(want_w), (5 + 18) * P.U32 * terms * 1.05, 0))
+
+
+@pytest.mark.parametrize("dim,rot,near,dtype,from_codes", [(8, 0, False, "f32", False), (7, 0, False, "bf16", False), (8, 2, True, "f16", True),
+                                                           (64, 64, False, "bf16", True), (128, 32, False, "bf16", False)])
+def test_long_sums_of_dweight(dim, rot, near, dtype, from_codes):
+    """dweight's error does not grow with the tokens: ones first, then terms of which a binary32 sum of one would take none."""
+    import torch
+    import optimizer_step_amd as osa
+    waves, each = 4096, 256
+    tokens, small = waves * each, 2.0 ** -25 if dtype != "f16" else 2.0 ** -24
+    dy = torch.full((tokens, 1, dim), small, dtype=P.TYPES[dtype], device="cuda")
+    dy[:waves] = 1
+    x = torch.ones(tokens, 1, dim, dtype=P.TYPES[dtype], device="cuda")
+    xin = x
+    if from_codes:
+        xin = osa.block_buffers(tokens, dim)
+        osa.opt_block_cast(x.view(tokens, dim), codes=xin)
+    dx = [torch.empty_like(x) for _ in range(2)]
+    dw = [torch.full((dim,), -5.0, device="cuda") for _ in range(2)]
+    table = osa.rotation_table(1, rot) if rot else None            # position 0: cos 1, sin 0
+    osa.opt_head_norm_backward(dy, dy, xin, xin, table=table, positions=torch.zeros(tokens, dtype=torch.int32, device="cuda"), eps=0.0,
+                               interleaved=near, dq=dx[0], dk=dx[1], dweight_q=dw[0], dweight_k=dw[1])
+    want = waves * (1 + (each - 1) * small)                        # r = 1: every term is dy's, exactly
+    for w in dw:
+        # 31 additions in binary32 at most before a sum is widened, half a step of 1 each; the result's rounding
+        assert bool(((w.double() - want).abs() <= 32 * P.U32 * want).all()), float(w[0])
