@@ -611,7 +611,7 @@ int opt_head_norm(const opt_heads *a, void *stream);
  *   dx = r * (g - x * (r^2 c)),
  *   dweight = sum over tokens and heads of dn * (x * r).
  * The sums over tokens run in a fixed order (no atomics): binary32 over at most
- * 32 heads in turn, binary64 from there on, rounded once to dweight.  dx may be
+ * four heads in turn, binary64 from there on, rounded once to dweight.  dx may be
  * dy with the same strides.  A token whose position the table does not hold gets
  * NaNs, and they reach dweight.  With no heads or tokens a dweight becomes 0 (or
  * stays, with accumulate). */

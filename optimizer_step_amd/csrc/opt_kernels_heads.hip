@@ -310,10 +310,10 @@ __global__ __launch_bounds__(kHeadThreads) void head_norm_kernel(HeadArgs, int)
     }
 }
 
-// The backward pass: a wave takes tokens in turn and keeps its sums of both
-// weights' gradients in registers, in binary32 over 32 units at most, then joins
-// them to its sums in the LDS, in binary64 from there on (all of a wave's sums in
-// binary64 registers would cost a wave a SIMD).
+// The backward pass: a wave takes tokens in turn.  A lane's sums of both weights'
+// gradients run in binary32 over the units it has in registers at once, four at
+// most, and join binary64 sums of its own in the LDS there (in registers they
+// would cost a wave a SIMD).
 constexpr int kHeadGradThreads = 256;
 constexpr int64_t kHeadGradGroups = 1024;    // four waves a SIMD; 512 measured 72 us against 55 at the sizes above
 
@@ -341,7 +341,7 @@ __device__ __forceinline__ void arrived(HeadIn<DT, true> (&x)[N])
     }
 }
 
-constexpr int kHeadFold = 32;
+constexpr int kSumRow = 72;        // 64 lanes' sums and a gap: eight rows fall into different banks by pairs
 
 template <int DT, bool CODED> constexpr int head_grad_most() { return DT == kP32 ? 2 : 4; }
 
@@ -349,31 +349,18 @@ template <int DT, int L, int MODE, bool CODED>
 __global__ __launch_bounds__(kHeadGradThreads) void head_norm_grad_kernel(HeadGradArgs)
 {
     constexpr int kWaves = kHeadGradThreads / 64, S = 64 / L, kSize = sizeof(typename Elem<DT>::T), kMost = head_grad_most<DT, CODED>();
-    __shared__ double comb[kWaves][2][L * 8];
+    __shared__ double comb[kWaves][2][8][kSumRow];     // a lane's sums of its columns 8 (l % L) + i
     __shared__ float lds[MODE == kAny ? kWaves * kWaveFloats : 1];
     const OPT_CONST HeadGradArgs *k = kernargs<HeadGradArgs>();
     const HeadTurn t = turn_of(k->t);
     const int lane = threadIdx.x % L, c = 8 * lane, slot = (threadIdx.x & 63) / L;
     const int cnt = left8(c, t.dim);
     const int wave = wave_id();
-    float dw[2][8] = {};
-    int summed = 0;        // units since the sums last joined the LDS's, where lane l < L owns columns 8 l on of its wave's
-    if (slot == 0)
+    const bool sums = k->part != nullptr;
+    double *const mine = &comb[wave][0][0][threadIdx.x & 63];
+    if (sums)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) comb[wave][0][c + i] = comb[wave][1][c + i] = 0.0;
-    auto join = [&] {
-        int at = c;
-        asm volatile("" : "+v"(at));               // no address is kept for this in the loop
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const double v = groups_sum<L>((double)dw[q][i]);
-                if (slot == 0) comb[wave][q][at + i] += v;
-                dw[q][i] = 0.0f;
-            }
-        summed = 0;
-    };
+        for (int i = 0; i < 16; ++i) mine[kSumRow * i] = 0.0;
     const int64_t step = (int64_t)gridDim.x * kWaves;
     const int headsq = (int)k->s[0].heads, headsk = (int)k->s[1].heads;
     const int unitsq = (headsq + S - 1) / S, units = unitsq + (headsk + S - 1) / S;
@@ -419,6 +406,7 @@ __global__ __launch_bounds__(kHeadGradThreads) void head_norm_grad_kernel(HeadGr
                 angles<MODE, true>(t, row, c, cs, sn);
             }
             arrived(in);
+            float dw[2][8] = {};
             const OPT_CONST HeadGradSet *h = k->s;
 #pragma unroll
             for (int j = 0; j < kMost; ++j) {
@@ -465,18 +453,25 @@ __global__ __launch_bounds__(kHeadGradThreads) void head_norm_grad_kernel(HeadGr
                     }
                 }
             }
-            summed += n;
-            if (summed > kHeadFold - kMost && k->part) join();
+            // the lane's own sums: an addition in the LDS, of which nothing is waited for
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (sums && (q ? first + n > unitsq : first < unitsq))
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        __hip_atomic_fetch_add(mine + kSumRow * (8 * q + i), (double)dw[q][i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         }
     }
-    if (!k->part) return;
-    // the workgroup's sums: its waves' in a fixed order
-    join();
+    if (!sums) return;
+    // the workgroup's sums, over the lanes that hold the same columns, in a fixed order
     __syncthreads();
     for (int e = threadIdx.x; e < 2 * t.dim; e += kHeadGradThreads) {
         const int q = e >= t.dim, j = e - q * t.dim;
-        double v = comb[0][q][j];
-        for (int w = 1; w < kWaves; ++w) v += comb[w][q][j];
+        double v = 0.0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+#pragma unroll
+            for (int l = 0; l < 64; l += L) v += comb[w][q][j & 7][(j >> 3) + l];
         gst<double>(k->part + ((int64_t)blockIdx.x * 2 + q) * t.dim + j, v);
     }
 }

@@ -337,16 +337,6 @@ __device__ __forceinline__ double lanes_sum(double x)
     return x;
 }
 
-// The rest of a wave's sum: over the 64/LANES lanes that are LANES apart.
-template <int LANES>
-__device__ __forceinline__ double groups_sum(double x)
-{
-    if (LANES <= 8) x = dpp_add<0x128>(x);
-    if (LANES <= 16) x = swap16_add(x);
-    if (LANES <= 32) x = swap32_add(x);
-    return x;
-}
-
 // 1/sqrt(x) to within 2^-51: the hardware's estimate and two Newton steps, a
 // tenth of the instructions of a division after a square root (each of which
 // every wave would run once a row: 33 -> 31 us of a pass over 8192 x 4096).
