@@ -473,8 +473,16 @@ __device__ __forceinline__ void grad_tile(const OPT_CONST GateGradArgs *a, TileL
     if (a->yt.codes) put_tile<SHAPE>(lds, 2, copy(a->yt), r0, c0, a->rows, a->cols);
 }
 
+// Waves a SIMD: four, in 128 registers, but two for 32-bit matrices (three operands
+// of 32 registers a thread) and for 32-bit dy beside codes where columns are no
+// multiple of eight (the code for single elements: 35 to 39 registers spilled in 128;
+// 8191 x 4100 SiLU 172 us, 157 with two).  With whole eights four measure better
+// though they spill 2 to 5 (8191 x 4104 from codes 111 us, 151 with two).
+template <int DT, bool CODED, int SHAPE>
+constexpr int grad_waves() { return DT == kP32 && (!CODED || SHAPE == kAnyShape) ? 2 : 4; }
+
 template <int DT, int ACT, bool CODED, int SHAPE>
-__global__ __launch_bounds__(kTileThreads, DT == kP32 && !CODED ? 2 : 4) void gated_act_grad_kernel(GateGradArgs)
+__global__ __launch_bounds__(kTileThreads, grad_waves<DT, CODED, SHAPE>()) void gated_act_grad_kernel(GateGradArgs)
 {
     __shared__ TileLds<3> lds;
     const OPT_CONST GateGradArgs *a = kernargs<GateGradArgs>();
