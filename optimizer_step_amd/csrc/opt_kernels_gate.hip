@@ -482,7 +482,7 @@ template <int DT, bool CODED, int SHAPE>
 constexpr int grad_waves() { return DT == kP32 && (!CODED || SHAPE == kAnyShape) ? 2 : 4; }
 
 template <int DT, int ACT, bool CODED, int SHAPE>
-__global__ __launch_bounds__(kTileThreads, grad_waves<DT, CODED, SHAPE>()) void gated_act_grad_kernel(GateGradArgs)
+__global__ __launch_bounds__(kTileThreads, (grad_waves<DT, CODED, SHAPE>())) void gated_act_grad_kernel(GateGradArgs)
 {
     __shared__ TileLds<3> lds;
     const OPT_CONST GateGradArgs *a = kernargs<GateGradArgs>();
