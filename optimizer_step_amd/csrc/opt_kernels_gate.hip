@@ -16,30 +16,36 @@
 
 namespace optstep {
 
-// sigma(p) and 1 - sigma(p).  FINE (32-bit results): each to a few binary32
-// units of itself.  Both come from e = exp(-|p|) <= 1, so neither overflows nor
-// cancels, and the rounding of |p| log2(e), which exp2 would make relative |p|
-// 2^-24 of e, is carried along (|p| held at 256, where e is 0, so that it is
-// finite).  16-bit and 8-bit results do not see those: there exp(-p) may reach
-// infinity, where sigma is 0, and 1 - sigma is good to 2^-23 of 1.  A NaN p may
-// give any values: its x makes them NaN.
-template <bool FINE>
-__device__ __forceinline__ void logistic(float p, float &sig, float &rest)
+// sigma(p) = sig * scale and rest = 1 - sigma(p).  FINE (32-bit results): each to a
+// few binary32 units of itself.  Both come from e = exp(-|p|) <= 1, so nothing
+// overflows or cancels, and what the rounding of |p| log2(e) costs, |p| 2^-24 of
+// e, is put back (SiLU's |p| is held at 256, where e is 0, so that it is finite;
+// GELU's is).  The hardware's exp2 gives 0 below 2^-126, where x e may still be a
+// normal number: below p = -64, where 1 + e is 1 either way, e is formed 2^24
+// times as large, and what sig makes is scaled back.
+// 16-bit and 8-bit results do not see those: there exp(-p) may reach infinity,
+// sigma is 0 below 2^-126, its exponent keeps the rounding of p log2(e), and 1 -
+// sigma is good to 2^-23 of 1.  A NaN p may give any values: its x makes them NaN.
+template <int ACT, bool FINE>
+__device__ __forceinline__ void logistic(float p, float &sig, float &rest, float &scale)
 {
     if (!FINE) {
         sig = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(p * -1.44269504f));
         rest = 1.0f - sig;
+        scale = 1.0f;
         return;
     }
-    const float a = __builtin_fminf(__builtin_fabsf(p), 256.0f);
+    const float a = ACT == kActSilu ? __builtin_fminf(__builtin_fabsf(p), 256.0f) : __builtin_fabsf(p);
     const float t = a * -1.44269504f;
-    float e = __builtin_amdgcn_exp2f(t);
-    // -a log2(e) = t + (its rounding + a times what the constant lacks)
-    const float lo = __builtin_fmaf(a, -1.92596299e-8f, __builtin_fmaf(a, -1.44269504f, -t));
-    e = __builtin_fmaf(e * 0.693147181f, lo, e);
+    const bool far = p < -64.0f;
+    float e = __builtin_amdgcn_exp2f(t + (far ? 24.0f : 0.0f));        // (the sum is exact)
+    // -a = t ln(2) + what t lacks
+    const float lack = __builtin_fmaf(t, 1.90465438e-9f, __builtin_fmaf(t, -0.693147182f, -a));
+    e = __builtin_fmaf(e, lack, e);
     const float big = __builtin_amdgcn_rcpf(1.0f + e), small = e * big;
     sig = p >= 0.0f ? big : small;
     rest = p >= 0.0f ? small : big;
+    scale = far ? 0x1p-24f : 1.0f;
 }
 
 // p(x) and p'(x).  GELU: beyond |x| = 16 exp(-|p|) is 0 in binary32, so x is
@@ -62,20 +68,21 @@ __device__ __forceinline__ void inner(float x, float &p, float &dp)
 template <int ACT, bool FINE>
 __device__ __forceinline__ float act(float x)
 {
-    float p, dp, sig, rest;
+    float p, dp, sig, rest, scale;
     inner<ACT>(x, p, dp);
-    logistic<FINE>(p, sig, rest);
-    return x * sig;
+    logistic<ACT, FINE>(p, sig, rest, scale);
+    return (x * sig) * scale;
 }
 
 template <int ACT, bool FINE>
 __device__ __forceinline__ void act_slope(float x, float &s, float &slope)
 {
-    float p, dp, sig, rest;
+    float p, dp, sig, rest, scale;
     inner<ACT>(x, p, dp);
-    logistic<FINE>(p, sig, rest);
+    logistic<ACT, FINE>(p, sig, rest, scale);
     s = x * sig;
-    slope = ACT == kActSilu ? __builtin_fmaf(s, rest, sig) : __builtin_fmaf(s * rest, dp, sig);
+    slope = (ACT == kActSilu ? __builtin_fmaf(s, rest, sig) : __builtin_fmaf(s * rest, dp, sig)) * scale;
+    s *= scale;
 }
 
 // One row's block of 128 columns by 16 lanes: codes and the scale's byte.

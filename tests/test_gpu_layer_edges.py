@@ -107,3 +107,27 @@ def test_long_sums_of_dweight(dim, rot, near, dtype, from_codes):
     for w in dw:
         # three additions in binary32 at most before a sum is widened, half a step of 1 each; the result's rounding
         assert bool(((w.double() - want).abs() <= 4 * P.U32 * want).all()), float(w[0])
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_far_gates_in_32_bits(act, monkeypatch):
+    """Where sigma is below the normal numbers, x sigma still is one: 32-bit results keep their units down to the subnormals."""
+    import torch
+    import optimizer_step_amd as osa
+    monkeypatch.setattr(G, "FLUSH", 2.0 ** -148)        # s, sigma and their products each off by half a subnormal at most
+    x = np.linspace(*((-104, -60) if act == "silu" else (-10.7, -8)), 8192).astype(np.float32).reshape(16, 512)
+    u, dy = (np.random.RandomState(i).uniform(0.5, 2, x.shape).astype(np.float32) for i in (1, 2))
+    want, bound = G.gate(x, u, act, "f32")
+    tail = (np.abs(want) > 2.0 ** -126) & (np.abs(want / u / x) < 2.0 ** -126)
+    assert tail.sum() > 100                             # normal results of a sigma that is none
+    y, dg, du = (torch.empty(16, 512, device="cuda") for _ in range(3))
+    osa.opt_gated_act(dev(x, "f32"), dev(u, "f32"), act, y=y)
+    osa.opt_gated_act_backward(dev(dy, "f32"), dev(x, "f32"), dev(u, "f32"), act, dgate=dg, dup=du)
+    (wg, bg), (wu, bu), _ = G.gate_gradients(dy, x, u, act, "f32")
+    for got, w, b in ((y, want, bound), (dg, wg, bg), (du, wu, bu)):
+        G.check_values(host(got), w, G.stored(w, b, "f32"))
+    # the tiles too
+    t = osa.block_buffers(512, 16)
+    osa.opt_gated_act_backward(dev(dy, "f32"), dev(x, "f32"), dev(u, "f32"), act, dgate=(a := torch.empty_like(dg)), dup=(b := torch.empty_like(du)),
+                               y_codes_t=t)
+    assert torch.equal(a, dg) and torch.equal(b, du)
