@@ -131,3 +131,25 @@ def test_far_gates_in_32_bits(act, monkeypatch):
     osa.opt_gated_act_backward(dev(dy, "f32"), dev(x, "f32"), dev(u, "f32"), act, dgate=(a := torch.empty_like(dg)), dup=(b := torch.empty_like(du)),
                                y_codes_t=t)
     assert torch.equal(a, dg) and torch.equal(b, du)
+
+
+def test_slope_beside_a_saturated_gate():
+    """16-bit dgate = u s'(x) rounds to the exact value's neighbour where that is 7 to 25 units of binary32 from a tie: its binary32
+    form is off by 3 (1 + e, the reciprocal), 0.7 (the tail s (1 - sigma) p', below 0.013 and off by 50 units of itself), 1 (their
+    sum) and 1 (the product with u).  1 - sigma formed by a subtraction would be off by 3 units of 1, of which the tail makes 10 to 25 times as many."""
+    import torch
+    import optimizer_step_amd as osa
+    x = np.arange(3, 4.5, 2.0 ** -8)
+    u = np.arange(1, 2, 2.0 ** -10)
+    x, u = (v.reshape(-1) for v in np.meshgrid(x, u))
+    (want, _), _, _ = G.gate_gradients(np.ones_like(x), x, u, "gelu", "f16")
+    step = 2.0 ** (np.floor(np.log2(want)) - 10)
+    off = np.abs(want / step - np.floor(want / step) - 0.5) * step / want / P.U32
+    near = (off > 7) & (off < 25)
+    assert near.sum() > 1000
+    x, u, want = (v[near][:near.sum() // 128 * 128].reshape(-1, 128) for v in (x, u, want))
+    dg, tile = (torch.empty(*x.shape, dtype=torch.float16, device="cuda") for _ in range(2))
+    one = torch.ones_like(dg)
+    osa.opt_gated_act_backward(one, dev(x, "f16"), dev(u, "f16"), "gelu", dgate=dg)
+    osa.opt_gated_act_backward(one, dev(x, "f16"), dev(u, "f16"), "gelu", dgate=tile, y_codes_t=osa.block_buffers(128, x.shape[0]))
+    assert np.array_equal(host(dg), want.astype(np.float16).astype(np.float32)) and torch.equal(dg, tile)
