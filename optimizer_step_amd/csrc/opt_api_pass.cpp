@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <initializer_list>
 
 #include "opt_pass.h"
 #include "opt_step.h"
@@ -89,6 +90,18 @@ int check_more(const char *what, const void *p, int64_t ld, int64_t rows, int64_
 int check_more(const char *what, const opt_codes &q, int64_t rows, int64_t bytes)
 {
     return q.codes ? check_codes(what, q, rows, bytes) : OPT_OK;
+}
+
+// Coded outputs of one call: each in buffers of its own.
+int check_apart(std::initializer_list<const opt_codes *> out)
+{
+    for (const opt_codes *a : out)
+        for (const opt_codes *b : out) {
+            if (a == b) break;
+            if (a->codes && b->codes && (a->codes == b->codes || a->scales == b->scales))
+                return report(OPT_EINVAL, "two coded results have the same buffer");
+        }
+    return OPT_OK;
 }
 
 int check_act(int32_t act)
@@ -364,6 +377,7 @@ int opt_gated_act(const opt_gate *n, void *stream)
     if ((rc = check_more("q", n->q, n->rows, n->cols)) != OPT_OK) return rc;
     if ((rc = check_more("gate_q", n->gate_q, n->rows, n->cols)) != OPT_OK) return rc;
     if ((rc = check_more("up_q", n->up_q, n->rows, n->cols)) != OPT_OK) return rc;
+    if ((rc = check_apart({&n->q, &n->gate_q, &n->up_q})) != OPT_OK) return rc;
     GateArgs a{};
     a.rows = n->rows;
     a.cols = n->cols;
@@ -407,6 +421,9 @@ int opt_gated_act_backward(const opt_gate_grad *n, void *stream)
     if ((rc = check_more("dgate_t", n->dgate_t, n->cols, n->rows)) != OPT_OK) return rc;
     if ((rc = check_more("dup_t", n->dup_t, n->cols, n->rows)) != OPT_OK) return rc;
     if ((rc = check_more("y_t", n->y_t, n->cols, n->rows)) != OPT_OK) return rc;
+    if ((rc = check_apart({&n->dgate_q, &n->dup_q, &n->dgate_t, &n->dup_t, &n->y_t})) != OPT_OK) return rc;
+    for (const opt_codes *in : {&n->gate_q, &n->up_q})
+        if ((rc = check_apart({&n->dgate_t, &n->dup_t, &n->y_t, in})) != OPT_OK) return rc;
     GateGradArgs a{};
     a.rows = n->rows;
     a.cols = n->cols;
@@ -482,6 +499,10 @@ int opt_head_norm(const opt_heads *n, void *stream)
         d.q = codes_of(s.codes);
     }
     if (n->tokens == 0 || heads == 0) return OPT_OK;
+    if (n->q.heads && n->k.heads) {
+        if (n->q.y == n->k.y) return report(OPT_EINVAL, "the two y must be different");
+        if ((rc = check_apart({&n->q.codes, &n->k.codes})) != OPT_OK) return rc;
+    }
     if ((rc = check_table(n->table, n->tokens, n->rot)) != OPT_OK) return rc;
     a.t = turn_of(n->tokens, n->dim, n->rot, n->w_dtype, n->interleaved, n->eps, n->table);
     return done(launch_head_norm(n->dtype, a, (hipStream_t)stream), "head norm launch");
@@ -541,6 +562,7 @@ int opt_head_norm_backward(const opt_heads_grad *n, void *stream)
         d.dxh = s.dx_head;
         d.q = codes_of(s.codes);
     }
+    if (n->tokens > 0 && n->q.heads && n->k.heads && n->q.dx == n->k.dx) return report(OPT_EINVAL, "the two dx must be different");
     if (coded && plain) return report(OPT_EINVAL, "q and k are both given as matrices or both as codes");
     if (n->q.dweight && n->q.dweight == n->k.dweight) return report(OPT_EINVAL, "the two dweights must be different");
     const bool any = n->tokens > 0 && heads > 0, sums = n->q.dweight || n->k.dweight;

@@ -1,0 +1,33 @@
+"""Host-side checks of what the operators between a layer's products refuse: results
+that share a buffer, results over inputs that are laid out otherwise, and what the
+binding would leave out.  Made-up addresses: every refused call ends before any
+device work."""
+import pytest
+import torch
+
+from tests.test_layer_cpu import EINVAL, L, codes, gate, gate_grad, heads, heads_grad  # noqa: F401 (L: a fixture)
+
+
+def test_results_in_one_buffer(L):
+    """Two results of a call in one buffer are refused: codes or scales alone too, the queries' and the keys' as well."""
+    c = codes(L, ld=112, lds=100)
+    for other in (c, codes(L, codes=1 << 24, ld=112, lds=100), codes(L, scales=1 << 24, ld=112, lds=100)):
+        one = dict(rows=100)
+        for pair in (("q", "gate_q"), ("q", "up_q"), ("gate_q", "up_q")):
+            assert gate(L, **one, **dict(zip(pair, (c, other)))) == EINVAL
+            assert "same buffer" in L.opt_last_error()
+        outs = ("dgate_q", "dup_q", "dgate_t", "dup_t", "y_t")
+        for i, a in enumerate(outs):
+            for b in outs[:i]:
+                assert gate_grad(L, **one, **{a: c, b: other}) == EINVAL
+                assert "same buffer" in L.opt_last_error()
+        for a in outs[2:]:
+            for b in ("gate_q", "up_q"):
+                assert gate_grad(L, True, **one, **{b: c, a: other, "up_q" if b == "gate_q" else "gate_q": codes(L, 1 << 25, 112, 1 << 26, 100)}) == EINVAL
+                assert "same buffer" in L.opt_last_error()
+        assert heads(L, q=dict(codes=c), k=dict(codes=other)) == EINVAL
+        assert "same buffer" in L.opt_last_error()
+    assert heads(L, q=dict(y=1 << 27), k=dict(y=1 << 27)) == EINVAL
+    assert "two y" in L.opt_last_error()
+    assert heads_grad(L, q=dict(dx=1 << 27), k=dict(dx=1 << 27)) == EINVAL
+    assert "two dx" in L.opt_last_error()
