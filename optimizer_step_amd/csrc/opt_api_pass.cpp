@@ -104,6 +104,20 @@ int check_apart(std::initializer_list<const opt_codes *> out)
     return OPT_OK;
 }
 
+// A result over an input lies as the input does: elsewhere a workgroup would
+// write what another still reads.
+int check_over(const char *what, const void *out, int64_t ldo, const void *in, int64_t ldi, int64_t rows)
+{
+    if (out && out == in && rows > 1 && ldo != ldi) return report(OPT_EINVAL, "%s over an input must have its leading dimension", what);
+    return OPT_OK;
+}
+
+int check_over(const char *what, const void *out, int64_t ot, int64_t oh, const void *in, int64_t it, int64_t ih, int64_t tokens, int64_t heads)
+{
+    if (out == in && ((tokens > 1 && ot != it) || (heads > 1 && oh != ih))) return report(OPT_EINVAL, "%s over an input must have its strides", what);
+    return OPT_OK;
+}
+
 int check_act(int32_t act)
 {
     return act == OPT_SILU || act == OPT_GELU ? OPT_OK : report(OPT_EINVAL, "unknown activation %d", act);
@@ -378,6 +392,8 @@ int opt_gated_act(const opt_gate *n, void *stream)
     if ((rc = check_more("gate_q", n->gate_q, n->rows, n->cols)) != OPT_OK) return rc;
     if ((rc = check_more("up_q", n->up_q, n->rows, n->cols)) != OPT_OK) return rc;
     if ((rc = check_apart({&n->q, &n->gate_q, &n->up_q})) != OPT_OK) return rc;
+    if ((rc = check_over("y", n->y, n->ldy, n->gate, n->ldg, n->rows)) != OPT_OK) return rc;
+    if ((rc = check_over("y", n->y, n->ldy, n->up, n->ldu, n->rows)) != OPT_OK) return rc;
     GateArgs a{};
     a.rows = n->rows;
     a.cols = n->cols;
@@ -424,6 +440,12 @@ int opt_gated_act_backward(const opt_gate_grad *n, void *stream)
     if ((rc = check_apart({&n->dgate_q, &n->dup_q, &n->dgate_t, &n->dup_t, &n->y_t})) != OPT_OK) return rc;
     for (const opt_codes *in : {&n->gate_q, &n->up_q})
         if ((rc = check_apart({&n->dgate_t, &n->dup_t, &n->y_t, in})) != OPT_OK) return rc;
+    const void *const in[3] = {n->dy, n->gate, n->up};
+    const int64_t ld[3] = {n->lddy, n->ldg, n->ldu};
+    for (int i = 0; i < 3; ++i) {
+        if ((rc = check_over("dgate", n->dgate, n->lddg, in[i], ld[i], n->rows)) != OPT_OK) return rc;
+        if ((rc = check_over("dup", n->dup, n->lddu, in[i], ld[i], n->rows)) != OPT_OK) return rc;
+    }
     GateGradArgs a{};
     a.rows = n->rows;
     a.cols = n->cols;
@@ -487,6 +509,7 @@ int opt_head_norm(const opt_heads *n, void *stream)
         if ((rc = check_heads(names[i][2], s.y, s.y_token, s.y_head, n->tokens, s.heads, n->dim, size, true)) != OPT_OK) return rc;
         if ((rc = check_more(names[i][3], s.weight, n->dim, 1, n->dim, size_of(n->w_dtype))) != OPT_OK) return rc;
         if ((rc = check_more(names[i][0], s.codes, n->tokens * s.heads, n->dim)) != OPT_OK) return rc;
+        if ((rc = check_over(names[i][2], s.y, s.y_token, s.y_head, s.x, s.x_token, s.x_head, n->tokens, s.heads)) != OPT_OK) return rc;
         HeadSet &d = a.s[i];
         d.heads = s.heads;
         d.x = s.x;
@@ -501,6 +524,7 @@ int opt_head_norm(const opt_heads *n, void *stream)
     if (n->tokens == 0 || heads == 0) return OPT_OK;
     if (n->q.heads && n->k.heads) {
         if (n->q.y == n->k.y) return report(OPT_EINVAL, "the two y must be different");
+        if (n->q.y == n->k.x || n->k.y == n->q.x) return report(OPT_EINVAL, "y must not lie over the other set's x");
         if ((rc = check_apart({&n->q.codes, &n->k.codes})) != OPT_OK) return rc;
     }
     if ((rc = check_table(n->table, n->tokens, n->rot)) != OPT_OK) return rc;
@@ -547,6 +571,7 @@ int opt_head_norm_backward(const opt_heads_grad *n, void *stream)
         if ((rc = check_heads(names[i][2], s.dy, s.dy_token, s.dy_head, n->tokens, s.heads, n->dim, size, false)) != OPT_OK) return rc;
         if ((rc = check_heads(names[i][3], s.dx, s.dx_token, s.dx_head, n->tokens, s.heads, n->dim, size, true)) != OPT_OK) return rc;
         if (s.dx == s.x) return report(OPT_EINVAL, "dx and x must be different");
+        if ((rc = check_over(names[i][3], s.dx, s.dx_token, s.dx_head, s.dy, s.dy_token, s.dy_head, n->tokens, s.heads)) != OPT_OK) return rc;
         if ((rc = check_more(names[i][4], s.weight, n->dim, 1, n->dim, size_of(n->w_dtype))) != OPT_OK) return rc;
         HeadGradSet &d = a.s[i];
         d.heads = s.heads;
@@ -562,7 +587,11 @@ int opt_head_norm_backward(const opt_heads_grad *n, void *stream)
         d.dxh = s.dx_head;
         d.q = codes_of(s.codes);
     }
-    if (n->tokens > 0 && n->q.heads && n->k.heads && n->q.dx == n->k.dx) return report(OPT_EINVAL, "the two dx must be different");
+    if (n->tokens > 0 && n->q.heads && n->k.heads) {
+        if (n->q.dx == n->k.dx) return report(OPT_EINVAL, "the two dx must be different");
+        if (n->q.dx == n->k.dy || n->q.dx == n->k.x || n->k.dx == n->q.dy || n->k.dx == n->q.x)
+            return report(OPT_EINVAL, "dx must not lie over the other set's dy or x");
+    }
     if (coded && plain) return report(OPT_EINVAL, "q and k are both given as matrices or both as codes");
     if (n->q.dweight && n->q.dweight == n->k.dweight) return report(OPT_EINVAL, "the two dweights must be different");
     const bool any = n->tokens > 0 && heads > 0, sums = n->q.dweight || n->k.dweight;

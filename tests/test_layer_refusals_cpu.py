@@ -31,3 +31,28 @@ def test_results_in_one_buffer(L):
     assert "two y" in L.opt_last_error()
     assert heads_grad(L, q=dict(dx=1 << 27), k=dict(dx=1 << 27)) == EINVAL
     assert "two dx" in L.opt_last_error()
+
+
+def test_results_over_inputs(L):
+    """A result over an input is refused where their strides differ, or where it is the other set's."""
+    for p in (4096, 8192):
+        assert gate(L, y=p, ldy=101) == EINVAL
+        assert "leading dimension" in L.opt_last_error()
+    for out, ld in (("dgate", "lddg"), ("dup", "lddu")):
+        for p in (4096, 8192, 12288):
+            assert gate_grad(L, **{out: p, ld: 101}) == EINVAL
+            assert "leading dimension" in L.opt_last_error()
+        assert gate_grad(L, True, **{out: 4096, ld: 101}) == EINVAL
+        assert "leading dimension" in L.opt_last_error()
+    x = 1 << 14
+    for kw in (dict(y_token=193), dict(y_token=200, y_head=65), dict(y_token=64, y_head=320)):
+        assert heads(L, q=dict(y=x, **kw)) == EINVAL
+        assert "strides" in L.opt_last_error()
+        assert heads_grad(L, q=dict(dx=x, **{"d" + k.replace("y", "x"): v for k, v in kw.items()})) == EINVAL
+        assert "strides" in L.opt_last_error()
+    for kw in (dict(q=dict(y=1 << 16)), dict(k=dict(y=x))):
+        assert heads(L, **kw) == EINVAL
+        assert "other set" in L.opt_last_error()
+    for kw in (dict(q=dict(dx=1 << 16)), dict(q=dict(dx=(1 << 16) + (1 << 11))), dict(k=dict(dx=x)), dict(k=dict(dx=x + (1 << 11)))):
+        assert heads_grad(L, **kw) == EINVAL
+        assert "other set" in L.opt_last_error()
