@@ -909,6 +909,8 @@ def opt_head_norm(q, k, weight_q=None, weight_k=None, table=None, positions=None
     _on_device(q, "q", dev)
     if q.dim() != 3:
         raise ValueError("q must be [tokens, heads, dim]")
+    if k is None and (k_out is not None or k_codes is not None):
+        raise ValueError("k_out and k_codes need k")
     shape, dtype = q.shape, q.dtype
     tokens, heads, dim = shape
     tab, rot = _head_table(table, positions, tokens, dev)

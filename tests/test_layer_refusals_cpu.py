@@ -56,3 +56,12 @@ def test_results_over_inputs(L):
     for kw in (dict(q=dict(dx=1 << 16)), dict(q=dict(dx=(1 << 16) + (1 << 11))), dict(k=dict(dx=x)), dict(k=dict(dx=x + (1 << 11)))):
         assert heads_grad(L, **kw) == EINVAL
         assert "other set" in L.opt_last_error()
+
+
+def test_keys_results_need_keys(L, monkeypatch):
+    """The binding refuses results of keys that are not given, forward as backward."""
+    monkeypatch.setattr(L, "_device", lambda: -1)       # a host tensor's device number
+    h = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    for kw in (dict(k_out=h), dict(k_codes=L.block_buffers(8, 64, device="cpu"))):
+        with pytest.raises(ValueError, match="need k"):
+            L.opt_head_norm(h, None, q_out=h, **kw)
