@@ -831,6 +831,8 @@ def rotation_table(positions, rot, base=10000.0, device="cuda"):
     positions p < positions: float32 [positions, rot], the cosines first, each
     formed in binary64 and rounded once."""
     import torch
+    if rot < 0 or rot % 2:
+        raise ValueError(f"rot must be even and not negative, got {rot}")
     f = base ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
     a = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * f
     return torch.cat([a.cos(), a.sin()], 1).float()

@@ -65,3 +65,11 @@ def test_keys_results_need_keys(L, monkeypatch):
     for kw in (dict(k_out=h), dict(k_codes=L.block_buffers(8, 64, device="cpu"))):
         with pytest.raises(ValueError, match="need k"):
             L.opt_head_norm(h, None, q_out=h, **kw)
+
+
+def test_rotation_table_of_odd_size(L):
+    """A table has rot columns or is refused (an odd rot gave one more)."""
+    for rot in (1, 63, -2):
+        with pytest.raises(ValueError, match="even"):
+            L.rotation_table(9, rot, device="cpu")
+    assert L.rotation_table(9, 0, device="cpu").shape == (9, 0)
