@@ -541,7 +541,7 @@ int64_t opt_head_norm_workspace(int64_t tokens, int64_t heads_q, int64_t heads_k
     if (dim < 1) return report(OPT_EINVAL, "dim must be positive");
     if (dim > kMaxHeadDim) return report(OPT_EUNSUPPORTED, "heads above %d elements", kMaxHeadDim);
     if (tokens == 0 || heads_q + heads_k == 0) return 0;
-    return head_grad_groups(tokens, heads_q, heads_k, dim) * 2 * dim * (int64_t)sizeof(double);
+    return head_grad_groups(tokens) * 2 * dim * (int64_t)sizeof(double);
 }
 
 int opt_head_norm_backward(const opt_heads_grad *n, void *stream)
@@ -598,7 +598,7 @@ int opt_head_norm_backward(const opt_heads_grad *n, void *stream)
     if (any) {
         if ((rc = check_table(n->table, n->tokens, n->rot)) != OPT_OK) return rc;
         if (sums) {
-            const int64_t need = head_grad_groups(n->tokens, n->q.heads, n->k.heads, n->dim) * 2 * n->dim * (int64_t)sizeof(double);
+            const int64_t need = head_grad_groups(n->tokens) * 2 * n->dim * (int64_t)sizeof(double);
             if (!n->workspace) return report(OPT_EINVAL, "dweight needs a workspace");
             if (!at(n->workspace, 16)) return report(OPT_EALIGN, "the workspace must be 16-byte aligned");
             if (n->workspace_bytes < need)

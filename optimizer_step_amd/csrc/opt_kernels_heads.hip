@@ -343,12 +343,12 @@ __device__ __forceinline__ void arrived(HeadIn<DT, true> (&x)[N])
 
 constexpr int kSumRow = 72;        // 64 lanes' sums and a gap: eight rows fall into different banks by pairs
 
-template <int DT, bool CODED> constexpr int head_grad_most() { return DT == kP32 ? 2 : 4; }
+template <int DT> constexpr int head_grad_most() { return DT == kP32 ? 2 : 4; }
 
 template <int DT, int L, int MODE, bool CODED>
 __global__ __launch_bounds__(kHeadGradThreads) void head_norm_grad_kernel(HeadGradArgs)
 {
-    constexpr int kWaves = kHeadGradThreads / 64, S = 64 / L, kSize = sizeof(typename Elem<DT>::T), kMost = head_grad_most<DT, CODED>();
+    constexpr int kWaves = kHeadGradThreads / 64, S = 64 / L, kSize = sizeof(typename Elem<DT>::T), kMost = head_grad_most<DT>();
     __shared__ double comb[kWaves][2][8][kSumRow];     // a lane's sums of its columns 8 (l % L) + i
     __shared__ float lds[MODE == kAny ? kWaves * kWaveFloats : 1];
     const OPT_CONST HeadGradArgs *k = kernargs<HeadGradArgs>();
@@ -512,7 +512,7 @@ static int mode_of(const HeadTurn &t)
     return t.rot % 16 != 0 ? kAny : t.dim == 8 * head_lanes(t.dim) ? kWhole : kHalves;
 }
 
-int64_t head_grad_groups(int64_t tokens, int64_t heads_q, int64_t heads_k, int dim)
+int64_t head_grad_groups(int64_t tokens)
 {
     constexpr int kWaves = kHeadGradThreads / 64;
     const int64_t n = (tokens + kWaves - 1) / kWaves;
@@ -543,7 +543,7 @@ static hipError_t launch_head_t(const HeadArgs &a, hipStream_t st)
 template <int DT, int L, bool CODED>
 static hipError_t launch_head_grad_t(const HeadGradArgs &a, hipStream_t st)
 {
-    const unsigned grid = (unsigned)head_grad_groups(a.t.tokens, a.s[0].heads, a.s[1].heads, a.t.dim);
+    const unsigned grid = (unsigned)head_grad_groups(a.t.tokens);
     switch (mode_of(a.t)) {
     case kWhole: hipLaunchKernelGGL((head_norm_grad_kernel<DT, L, kWhole, CODED>), dim3(grid), dim3(kHeadGradThreads), 0, st, a); break;
     case kHalves: hipLaunchKernelGGL((head_norm_grad_kernel<DT, L, kHalves, CODED>), dim3(grid), dim3(kHeadGradThreads), 0, st, a); break;
@@ -592,7 +592,7 @@ hipError_t launch_head_norm_grad(int dt, int coded, const HeadGradArgs &a, float
         e = dt == kP32 ? launch_head_grad_dt<kP32, false>(a, st) : dt == kPBF16 ? launch_head_grad_dt<kPBF16, false>(a, st) : launch_head_grad_dt<kPF16, false>(a, st);
     }
     if (e != hipSuccess || (!dwq && !dwk)) return e;
-    const int64_t groups = any ? head_grad_groups(a.t.tokens, a.s[0].heads, a.s[1].heads, a.t.dim) : 0;
+    const int64_t groups = any ? head_grad_groups(a.t.tokens) : 0;
     hipLaunchKernelGGL(head_dw_kernel, dim3((unsigned)((2 * a.t.dim + 15) / 16)), dim3(1024), 0, st, (const double *)a.part, groups, a.t.dim, dwq, dwk,
                        accumulate);
     return hipGetLastError();

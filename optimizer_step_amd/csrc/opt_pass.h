@@ -133,7 +133,9 @@ struct HeadGradArgs {
     double *part;          // [groups][2][dim] partial sums of the weights' gradients, or null
 };
 
-int64_t head_grad_groups(int64_t tokens, int64_t heads_q, int64_t heads_k, int dim);
+// Workgroups of the heads' backward pass, by the tokens alone (so that the order
+// of the weights' sums is too).
+int64_t head_grad_groups(int64_t tokens);
 
 // Lanes of a row and workgroups of the norm's backward pass, by the shape
 // alone (so that the weight gradient's order of addition is too).
