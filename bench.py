@@ -259,6 +259,15 @@ class Row:
                 "samples_ms": [round(x, 4) for x in per]}
 
 
+def brief(rec):
+    """A row's record for the result line: the samples' median and p10/p90
+    without the samples, numbers to six digits, nothing that the workload's name
+    says, so that the line with every row stays below the 9 KB that a reader of
+    the last lines is sure to have (stderr has each round's median)."""
+    return {k: float(f"{v:.6g}") if isinstance(v, float) else v for k, v in rec.items()
+            if k not in ("samples_ms", "launch_ms", "tensors", "rounds", "round_medians_ms", "format", "optimizer", "p_dtype")}
+
+
 def time_workload(name, steps, warmup, torch, osa, synth):
     """One row on its own: build, W warmup and K timed steps, free."""
     row = Row(name, torch, osa, synth)
@@ -798,7 +807,7 @@ def main():
             {k: head_rounds[k] for k in ("steps", "ms_median", "ms_p10", "ms_p90", "achieved_GBps",
                                          "frac_of_peak", "round_medians_ms", "rounds")},
         "calibration": calib,
-        "rows": protocol[1:],
+        "rows": [brief(r) for r in protocol[1:]],
     }
     print(json.dumps(out), flush=True)
 
