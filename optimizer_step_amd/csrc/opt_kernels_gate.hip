@@ -6,12 +6,14 @@
 // 2 sqrt(2/pi) (x + 0.044715 x^3) the tanh form of GELU (0.5 (1 + tanh(z)) =
 // sigma(2 z)).  s'(x) = sigma (1 + x (1 - sigma) p'(x)).
 //
-// All are bound by HBM.  8192 x 11008 bf16, SiLU: forward to codes with both
-// inputs' codes 106 us (634 MB, 6.0 TB/s; the vector units are busy 70 % of the
-// time); backward from those codes to both gradients' codes in both layouts and
-// y's transposed 172 us (818 MB, 4.8 TB/s; a plain stream of four bytes in and
-// five out takes 141).  2047 x 4096 fp16 from and to matrices 14.8 us; 8192 x 4096
-// codes restored as the transpose's 11.9 us (68 MB).
+// Bound by HBM where rows are whole eights.  8192 x 11008 bf16, SiLU: forward to
+// codes with both inputs' codes 106 us (634 MB, 6.0 TB/s; the vector units are busy
+// 70 % of the time); backward from those codes to both gradients' codes in both
+// layouts and y's transposed 173 us (818 MB, 4.7 TB/s; a plain stream of four bytes
+// in and five out takes 141).  2047 x 4096 fp16 from and to matrices 14.9 us; 8192 x
+// 4096 codes restored as the transpose's 11.9 us (68 MB).  Sides that are no
+// multiples, 8191 x 11005 bf16: from codes 177 us; GELU from matrices 231 (995 MB,
+// 4.3 TB/s).  fp32, 8192 x 4096: from codes 82 us (4.5 TB/s), from matrices 141 (4.0).
 #include "opt_pass.h"
 
 namespace optstep {
@@ -179,8 +181,10 @@ __global__ __launch_bounds__(256) void gated_act_grad_rows_kernel(GateGradArgs a
 // ---- tiles of 128 x 128 whose transpose is coded too -----------------------
 // 512 threads: thread t holds the eight columns of group t % 16 in the four
 // rows of group t / 16.  The backward pass forms dgate first, then dup and y
-// together from the inputs again, which stay as they are stored: 128 registers
-// and two workgroups a compute unit.  Beside 165 to 169 us in the same runs: all
+// together from the inputs again, which stay as they are stored: 16-bit types in
+// 128 registers, two workgroups a compute unit (GELU from matrices with sides that
+// are no multiples of 128 spills one or two).  Whole tiles of bf16 from codes beside
+// 165 to 169 us in the same runs: all
 // three held at once (250 registers, one workgroup) 230, or in 128 registers 642
 // (spills); s(gate) kept from part to part for two rows 175 (spills); every thread
 // forming its columns' scales, one barrier less a part, 171; a persistent grid
@@ -485,8 +489,8 @@ __device__ __forceinline__ void grad_tile(const OPT_CONST GateGradArgs *a, TileL
 
 // Waves a SIMD: four, in 128 registers, but two for 32-bit matrices (three operands
 // of 32 registers a thread) and for 32-bit dy beside codes where columns are no
-// multiple of eight (the code for single elements: 35 to 39 registers spilled in 128;
-// 8191 x 4100 SiLU 172 us, 157 with two).  With whole eights four measure better
+// multiple of eight (the code for single elements: 37 to 41 registers spilled in 128;
+// 8191 x 4100 SiLU 175 us, 157 with two).  With whole eights four measure better
 // though they spill 2 to 5 (8191 x 4104 from codes 111 us, 151 with two).
 template <int DT, bool CODED, int SHAPE>
 constexpr int grad_waves() { return DT == kP32 && (!CODED || SHAPE == kAnyShape) ? 2 : 4; }

@@ -14,12 +14,13 @@
 // y = (x r) A + (x' r) B.
 //
 // Bound by HBM and by the latency of a wave's chain (position, table's row and
-// elements, sums, root).  8192 tokens of 32 + 8 heads of 128, bf16: forward with
-// codes 42 us (215 MB, 5.1 TB/s), without 36; backward from codes 48 us and 4 for
-// the sums of both weights' gradients (214 MB, 4.1 TB/s; the vector units are busy
-// half the time).  Stores carry the non-temporal hint (51.7 us forward without);
-// so do the loads where no codes are written (43.8 -> 37.9 us; with codes 43.9
-// -> 45.7) and the backward pass's (53.1 -> 51.1).
+// elements, sums, root).  A pass among others over 8192 tokens of 32 + 8 heads of
+// 128, bf16: forward with codes 41 us (215 MB, 5.3 TB/s; the vector units are busy
+// 55 % of the time), without 35; backward from codes 49 us (214 MB, 4.4 TB/s; 66 %),
+// of which the sums of both weights' gradients are 4.  Stores carry the
+// non-temporal hint (51.7 us forward without); so do the loads where no codes are
+// written (43.8 -> 37.9 us; with codes 43.9 -> 45.7) and the backward pass's (53.1
+// -> 51.1).
 #include "opt_pass.h"
 
 namespace optstep {
@@ -315,7 +316,9 @@ __global__ __launch_bounds__(kHeadThreads) void head_norm_kernel(HeadArgs, int)
 // most, and join binary64 sums of its own in the LDS there (in registers they
 // would cost a wave a SIMD).
 constexpr int kHeadGradThreads = 256;
-constexpr int64_t kHeadGradGroups = 1024;    // four waves a SIMD; 512 measured 72 us against 55 at the sizes above
+// Four waves a SIMD, which kWhole's registers allow (512 measured 72 us against 55
+// at the sizes above); the other forms hold three at once.
+constexpr int64_t kHeadGradGroups = 1024;
 
 // A lane's inputs of one head, as they are stored.
 template <int DT, bool CODED> struct HeadIn { Raw<DT> dy, x; };
