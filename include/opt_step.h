@@ -484,8 +484,9 @@ int opt_block_matmul(const opt_product *a, void *stream);
  * infinity.  With OPT_F32 s is good to a few binary32 units of itself down to the
  * subnormals (OPT_GELU: p to 5 units of its own).  With the 16-bit types, and the
  * codes made beside them, sigma and 1 - sigma keep the rounding of p's exponent,
- * up to |p| 2^-23 of themselves, and a sigma below 2^-126 (p below -87.3) is 0.  gate and up are two matrices, or the halves of one [rows, 2 cols]
- * (ldg = ldu = 2 cols). */
+ * up to |p| 2^-23 of themselves, and a sigma below 2^-126 (p below -87.3) is 0.
+ * gate and up are two matrices, or the halves of one [rows, 2 cols] (ldg = ldu =
+ * 2 cols). */
 #define OPT_SILU 0
 #define OPT_GELU 1
 

@@ -27,8 +27,9 @@ namespace optstep {
 // times as large, and what sig makes is scaled back.
 // 16-bit and 8-bit results do not see those: there exp(-p) may reach infinity, the
 // exponent keeps the rounding of p log2(e), and sigma is 0 below 2^-126 (rest too,
-// where it is multiplied by such a sigma).  To carry the rounding along there took
-// 112 us for 107 at 8192 x 11008 and changed none of its codes.
+// where it is multiplied by such a sigma).  To put the rounding back there took 112
+// us for 107 (8192 x 11008, forward) and left as many of the gradients' codes off the
+// exact ones as before.
 // A NaN p may give any values: its x makes them NaN.
 template <int ACT, bool FINE>
 __device__ __forceinline__ void logistic(float p, float &sig, float &rest, float &scale)

@@ -134,9 +134,10 @@ def test_far_gates_in_32_bits(act, monkeypatch):
 
 
 def test_slope_beside_a_saturated_gate():
-    """16-bit dgate = u s'(x) rounds to the exact value's neighbour where that is 7 to 25 units of binary32 from a tie: its binary32
-    form is off by 3 (1 + e, the reciprocal), 0.7 (the tail s (1 - sigma) p', below 0.013 and off by 50 units of itself), 1 (their
-    sum) and 1 (the product with u).  1 - sigma formed by a subtraction would be off by 3 units of 1, of which the tail makes 10 to 25 times as many."""
+    """16-bit dgate = u s'(x) rounds as the exact value does where that is 7 to 25 units of binary32 from a tie: its
+    binary32 form is off by 3 (1 + e, the reciprocal), 0.7 (the tail s (1 - sigma) p', below 0.013 and off by 50 units
+    of itself), 1 (their sum) and 1 (the product with u).  1 - sigma formed by a subtraction would be off by 3 units of
+    1, and the tail by 10 to 25 times as many."""
     import torch
     import optimizer_step_amd as osa
     x = np.arange(3, 4.5, 2.0 ** -8)
